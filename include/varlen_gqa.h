@@ -363,6 +363,187 @@ int attn_run_noalloc(int B_max, int s_max, int Hq, int Hkv, int D, int max_q,
                      const int32_t *cu_q, const int32_t *cu_k, void *out,
                      float *lse, void *stream);
 
+/* ------------------------------------------------- operators on the cache
+ *
+ * What a serving step does to a paged cache around its attention call, in
+ * order: attn_append_paged writes the new tokens (rotated), attn_run_paged
+ * attends, attn_key_weights_paged adds up what each cached key was given, and
+ * attn_evict_paged shortens sequences that passed their budget.  A ledger of
+ * two arrays [B_max, Hkv, ld], owned by the caller, goes along with the cache:
+ *
+ *   weight  fp32, the attention weight that key j of head hk has gathered
+ *   born    int32, the index among all tokens its sequence was ever given of
+ *           the token that key j belongs to (eviction changes the places of
+ *           keys, differently in each KV head)
+ *   ld      elements between heads, >= s_max; entries at and past a
+ *           sequence's length are neither read nor written
+ *   seen    device, int32 [B_max]: tokens each sequence was ever given, those
+ *           of the present call included
+ *
+ * Rotations are applied before a key is cached and attention does not depend
+ * on the order of its keys, so a key keeps its rotation wherever it moves.
+ */
+
+/* Element types of attn_rope_apply. */
+#define ATTN_DTYPE_BF16 0
+#define ATTN_DTYPE_F16 1
+#define ATTN_DTYPE_F32 2
+
+/* Which elements of a head form pair i of n: (i, i + n) or (2 i, 2 i + 1). */
+#define ATTN_ROPE_HALF 0
+#define ATTN_ROPE_INTERLEAVED 1
+
+typedef struct attn_rope_s *attn_rope_t;   /* opaque */
+
+/*
+ * attn_rope_create -- the table of a rotary embedding with several position
+ * axes (text; time, height and width of images and video).
+ *
+ *   D        head dimension, 2..256
+ *   n_pairs  rotated pairs, 1..D/2; elements [2 n_pairs, D) are left as they are
+ *   n_axes   position axes, 1..8
+ *   freq     host, [n_pairs]: radians per unit of position, finite (64-bit:
+ *            the angle of a far position is reduced exactly, see attn_rope_apply)
+ *   axis     host, [n_pairs]: which axis turns pair i, in [0, n_axes)
+ *   layout   ATTN_ROPE_HALF or ATTN_ROPE_INTERLEAVED
+ *   scale    factor on cosine and sine (1 for a pure rotation), finite
+ *
+ * Host only: makes no CUDA call and holds no device memory; one table serves
+ * every device, stream and thread.  Owned by the caller until
+ * attn_rope_destroy (launched or captured calls hold copies of it).
+ */
+int attn_rope_create(attn_rope_t *out, int D, int n_pairs, int n_axes, const double *freq, const int32_t *axis,
+                     int layout, float scale);
+void attn_rope_destroy(attn_rope_t rope);   /* NULL is ignored */
+
+/*
+ * attn_rope_apply -- rotate the heads of T tokens, asynchronous on `stream`,
+ * one kernel, capturable.
+ *
+ *   dtype    ATTN_DTYPE_*, of x and out
+ *   x, out   device, [T, H, D], heads contiguous within a token,
+ *            x_token_stride and out_token_stride (>= H * D) elements between
+ *            tokens; aligned to their element (16 bytes, strides too, for the
+ *            widest accesses).  out may be x itself (same stride) or lie apart
+ *            from it; any other overlap is ATTN_E_INVALID_ARG
+ *   pos      device, int32, position of token t on axis a at pos[a * pos_stride
+ *            + t]; any value, negative ones too; pos_stride >= T
+ *   grad     0: out = R x.  1: out = R^T x, the gradient with respect to the
+ *            input for a gradient x with respect to the output
+ *
+ * Pair (u, w) of token t turns by theta = pos[axis_i, t] freq_i into
+ * scale (u cos theta - w sin theta, u sin theta + w cos theta), the sign of
+ * theta flipped for grad.  Angles are reduced in 64-bit fixed point, products
+ * are formed in fp32 and rounded once.
+ */
+int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int64_t x_token_stride, int64_t T, int H,
+                    const int32_t *pos, int64_t pos_stride, int grad, void *out, int64_t out_token_stride,
+                    void *stream);
+
+/*
+ * attn_append_paged -- write the new tokens' keys and values into a paged
+ * cache, rotating queries and keys on the way; asynchronous on `stream`, one
+ * kernel, capturable.
+ *
+ *   rope     a table with D equal to the plan's, or NULL for no rotation (pos
+ *            is then unused and may be NULL)
+ *   q, k, v  device, bf16 [T_q, Hq | Hkv | Hkv, D], 16-byte aligned, heads
+ *            contiguous within a token, *_token_stride elements between tokens
+ *            (multiples of 8, at least a token's heads), so the parts of one
+ *            fused projection work.  q and q_out may both be NULL: only the
+ *            cache is written
+ *   T_q      rows of q, k, v and pos, >= cu_q[B_max]
+ *   q_out    device, bf16 [T_q, Hq, D] packed, 16-byte aligned: the rotated
+ *            queries, ready for attn_run_paged.  q itself where q is packed,
+ *            or apart from it
+ *   pos      as in attn_rope_apply, for the T_q tokens
+ *   k_cache .. bt_stride  as in attn_run_paged
+ *   cu_q, cu_k  as in attn_run_paged: cu_k's lengths COUNT the new tokens, and
+ *            query token qi of sequence b is its key Lk_b - Lq_b + qi
+ *
+ * Only rows covered by cu_q are written to q_out.  A sequence that breaks the
+ * plan's bounds sets the plan's sticky bit and nothing of it is written; a
+ * block-table entry outside the cache sets ATTN_DEV_ERR_PAGE and its keys are
+ * not stored; tokens with a negative key index (Lq_b > Lk_b) are rotated but
+ * not stored.  Two sequences must not share the pages that are written.
+ */
+int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void *q, int64_t q_token_stride, const void *k,
+                      int64_t k_token_stride, const void *v, int64_t v_token_stride, int64_t T_q, const int32_t *pos,
+                      int64_t pos_stride, void *q_out, void *k_cache, void *v_cache, int64_t page_stride,
+                      int64_t token_stride, int page_size, int num_pages, const int32_t *block_table, int bt_stride,
+                      const int32_t *cu_q, const int32_t *cu_k, void *stream);
+
+/*
+ * attn_key_weights -- add up the attention weight that each key is given: the
+ * column sums of the attention matrix.  Asynchronous on `stream`, capturable.
+ *
+ *   q, k, cu_q, cu_k  as in attn_run_strided (the same tensors, after
+ *            rotation); k_token_stride as there
+ *   lse      device, fp32 [T_q, Hq]: the call's attn_run* result
+ *   weight_in, weight_out  device, fp32 ledgers of leading dimension ld; in may
+ *            be NULL (nothing gathered yet), or out itself, or apart from it
+ *   decay    >= 0 and finite; 0 reads nothing of weight_in
+ *   seen, born  both NULL, or: the births of this call's keys are written
+ *
+ *   weight_out[b, hk, j] = (j < Lk - Lq ? decay * weight_in[b, hk, j] : 0) +
+ *       sum over query tokens qi and the G heads h of hk, j < n(qi), of
+ *       exp(s_{qi,h,j} - lse_{qi,h})                   for every j < Lk_b
+ *   born[b, hk, j] = seen_b - Lk_b + j                 for Lk - Lq <= j < Lk
+ *
+ * with s and n as for attn_run.  A row with lse = -inf adds nothing; keys of
+ * the present tokens (j >= Lk - Lq) start from zero whatever weight_in holds.
+ * Lq_b may be less than the tokens that were attended with: passing the last
+ * few queries of a long prompt weighs its keys by that window alone (the
+ * window's tokens then are the present ones).  A sequence that breaks the
+ * plan's bounds sets the plan's sticky bit and is left unwritten.  Sums run in
+ * a fixed order: repeated calls give the same bits.
+ */
+int attn_key_weights(attn_plan_t plan, const void *q, const void *k, int64_t k_token_stride, const int32_t *cu_q,
+                     const int32_t *cu_k, const float *lse, float decay, const float *weight_in, float *weight_out,
+                     int64_t ld, const int32_t *seen, int32_t *born, void *stream);
+
+/* attn_key_weights over a paged cache (arguments of the cache as in
+ * attn_run_paged; a table entry outside it sets ATTN_DEV_ERR_PAGE and its keys
+ * count as zeros). */
+int attn_key_weights_paged(attn_plan_t plan, const void *q, const void *k_cache, int64_t page_stride,
+                           int64_t token_stride, int page_size, int num_pages, const int32_t *block_table,
+                           int bt_stride, const int32_t *cu_q, const int32_t *cu_k, const float *lse, float decay,
+                           const float *weight_in, float *weight_out, int64_t ld, const int32_t *seen, int32_t *born,
+                           void *stream);
+
+/*
+ * attn_evict_paged -- cut each sequence of a paged cache to a budget, keeping
+ * in every KV head the keys of the highest weight.  Asynchronous on `stream`,
+ * one kernel, capturable.
+ *
+ *   keep     device, int32 [B_max]: the budget; sequence b keeps c = min(Lk_b,
+ *            max(0, keep_b)) keys
+ *   sink, recent  >= 0: keys born below `sink` or at and past seen_b - recent
+ *            are protected: they rank as weight +inf
+ *   weight, born  the ledger; weight_out, born_out: the ledger after the cut
+ *            (entries below c), each its input itself or apart from everything
+ *   k_cache .. bt_stride  as in attn_run_paged; rows move within the cache, so
+ *            a sequence must not share its pages
+ *   cu_k     device, int32 [B_max + 1]: the lengths before
+ *   cu_k_out device, int32 [B_max + 1], apart from cu_k: 0 and the prefix sums
+ *            of the lengths after (a sequence that breaks the plan's bounds
+ *            sets its sticky bit, is left as it is, and counts as 0 here)
+ *
+ * Per (b, hk): the c keys of the highest rank stay, a NaN weight ranking as
+ * -inf and ties going to the lowest place.  A kept key at a place below c
+ * stays there; the kept keys at places c and above move, in order, into the
+ * evicted places below c, in order.  With weight_out and born_out apart from
+ * the inputs a repeated call does the same again.  Rows and ledger entries at
+ * c and above are left as they were; the pages past ceil(c / page_size) are
+ * free.  A table entry outside the cache sets ATTN_DEV_ERR_PAGE and the moves
+ * from or to it are left out.  Plans with s_max > 2^20 get ATTN_E_UNSUPPORTED.
+ */
+int attn_evict_paged(attn_plan_t plan, const float *weight, const int32_t *born, const int32_t *seen,
+                     const int32_t *keep, int sink, int recent, float *weight_out, int32_t *born_out, int64_t ld,
+                     void *k_cache, void *v_cache, int64_t page_stride, int64_t token_stride, int page_size,
+                     int num_pages, const int32_t *block_table, int bt_stride, const int32_t *cu_k, int32_t *cu_k_out,
+                     void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,9 +25,13 @@ ATTN_DEV_ERR_Q_TOO_LONG = 0x2
 ATTN_DEV_ERR_K_TOO_LONG = 0x4
 ATTN_DEV_ERR_TIMEOUT = 0x8
 ATTN_DEV_ERR_PAGE = 0x10
+ATTN_DTYPE_BF16, ATTN_DTYPE_F16, ATTN_DTYPE_F32 = 0, 1, 2
+ATTN_ROPE_HALF, ATTN_ROPE_INTERLEAVED = 0, 1
 
 EXPORTED = ("attn_plan", "attn_plan_ex", "attn_plan_info", "attn_run", "attn_run_strided", "attn_run_paged",
-            "attn_merge_lse", "attn_check_error", "attn_destroy", "attn_strerror")
+            "attn_merge_lse", "attn_check_error", "attn_destroy", "attn_strerror", "attn_rope_create",
+            "attn_rope_destroy", "attn_rope_apply", "attn_append_paged", "attn_key_weights", "attn_key_weights_paged",
+            "attn_evict_paged")
 
 
 class Overrides(ctypes.Structure):
@@ -86,6 +90,25 @@ def lib() -> ctypes.CDLL:
         L.attn_destroy.restype = None
         L.attn_strerror.argtypes = [i]
         L.attn_strerror.restype = ctypes.c_char_p
+        f32 = ctypes.c_float
+        L.attn_rope_create.argtypes = [ctypes.POINTER(vp), i, i, i, ctypes.POINTER(ctypes.c_double),
+                                       ctypes.POINTER(ctypes.c_int32), i, f32]
+        L.attn_rope_create.restype = i
+        L.attn_rope_destroy.argtypes = [vp]
+        L.attn_rope_destroy.restype = None
+        L.attn_rope_apply.argtypes = [vp, i, vp, i64, i64, i, i32p, i64, i, vp, i64, vp]
+        L.attn_rope_apply.restype = i
+        cache = [i64, i64, i, i, i32p, i]            # page_stride, token_stride, page_size, num_pages, table, bt_stride
+        L.attn_append_paged.argtypes = ([vp, vp, vp, i64, vp, i64, vp, i64, i64, i32p, i64, vp, vp, vp] + cache +
+                                        [i32p, i32p, vp])
+        L.attn_append_paged.restype = i
+        ledger = [i32p, i32p, vp, f32, vp, vp, i64, i32p, i32p, vp]
+        L.attn_key_weights.argtypes = [vp, vp, vp, i64] + ledger
+        L.attn_key_weights.restype = i
+        L.attn_key_weights_paged.argtypes = [vp, vp, vp] + cache + ledger
+        L.attn_key_weights_paged.restype = i
+        L.attn_evict_paged.argtypes = [vp, vp, i32p, i32p, i32p, i, i, vp, i32p, i64, vp, vp] + cache + [i32p, i32p, vp]
+        L.attn_evict_paged.restype = i
         _lib = L
         return L
 
@@ -132,6 +155,116 @@ def _stream_ptr(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+_ROPE_DTYPES = {torch.bfloat16: ATTN_DTYPE_BF16, torch.float16: ATTN_DTYPE_F16, torch.float32: ATTN_DTYPE_F32}
+
+
+def _heads_strided(name, t, H, D, dev):
+    """Token stride of t [T, H, D] whose heads are contiguous within a token."""
+    s = t.stride()
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D or t.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor [T, {H}, {D}] of CUDA device {dev}")
+    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
+        raise ValueError(f"{name} must keep each token's heads contiguous (strides (s, D, 1), s >= H*D)")
+    return s[0] if t.shape[0] > 1 else max(s[0], H * D)
+
+
+def rope_table(n_pairs, sections=None, *, base=10000.0, restart=False):
+    """freqs, axes for Rope: pair i of n turns with base^(-i / n) radians per
+    position.  sections: pairs per axis, in order (None: one axis for all);
+    restart=True begins the frequencies anew in each section."""
+    sections = [n_pairs] if sections is None else list(sections)
+    if sum(sections) != n_pairs or min(sections) < 0:
+        raise ValueError("sections must add up to n_pairs")
+    axes = [a for a, n in enumerate(sections) for _ in range(n)]
+    if restart:
+        freqs = [float(base) ** (-i / n) for n in sections for i in range(n)]
+    else:
+        freqs = [float(base) ** (-i / n_pairs) for i in range(n_pairs)]
+    return freqs, axes
+
+
+class Rope:
+    """Rotary positions with several axes (attn_rope_create).
+
+    Rope(D, freqs, axes=None, *, n_axes=None, layout="half", scale=1.0):
+    pair i of a head of D elements turns by pos[axes[i]] * freqs[i] radians;
+    layout "half" pairs elements (i, i + n), "interleaved" (2 i, 2 i + 1);
+    elements past the 2 n paired ones stay as they are; scale multiplies the
+    cosines and sines.  Holds no device memory: one table serves every device
+    and stream."""
+
+    def __init__(self, D, freqs, axes=None, *, n_axes=None, layout="half", scale=1.0):
+        self._h = None
+        n = len(freqs)
+        axes = [0] * n if axes is None else [int(a) for a in axes]
+        if len(axes) != n:
+            raise ValueError("axes must name one axis for each frequency")
+        if layout not in ("half", "interleaved"):
+            raise ValueError('layout must be "half" or "interleaved"')
+        self.D, self.n_pairs, self.layout, self.scale = int(D), n, layout, float(scale)
+        self.n_axes = int(n_axes) if n_axes is not None else max(axes, default=0) + 1
+        h = ctypes.c_void_p()
+        rc = lib().attn_rope_create(ctypes.byref(h), self.D, n, self.n_axes,
+                                    (ctypes.c_double * max(n, 1))(*[float(f) for f in freqs]),
+                                    (ctypes.c_int32 * max(n, 1))(*axes),
+                                    ATTN_ROPE_HALF if layout == "half" else ATTN_ROPE_INTERLEAVED, self.scale)
+        _check(rc, "attn_rope_create")
+        self._h = h
+
+    @property
+    def handle(self):
+        return self._h
+
+    def _pos(self, pos, T, dev):
+        """Address and axis stride of pos [n_axes, T] (or [T] for one axis)."""
+        if pos.dim() == 1 and self.n_axes == 1:
+            pos = pos[None]
+        if pos.dtype != torch.int32 or pos.get_device() != dev or pos.dim() != 2 or pos.shape[0] != self.n_axes or \
+                pos.shape[1] != T or (T > 1 and pos.stride(1) != 1):
+            raise ValueError(f"pos must be int32 [{self.n_axes}, {T}] on CUDA device {dev}, unit stride over tokens")
+        return pos.data_ptr(), max(pos.stride(0), T) if self.n_axes == 1 else pos.stride(0)
+
+    def apply(self, x, pos, out=None, *, grad=False, stream=None):
+        """out = rope.apply(x, pos[, out, grad, stream]): rotate x [T, H, D]
+        (bf16, fp16 or fp32; heads contiguous within a token, token stride
+        free) by pos [n_axes, T] int32.  grad=True applies the transpose: x is
+        the gradient of a rotated tensor, out that of its input.  out may be x
+        itself; it is allocated packed when not given."""
+        if self._h is None:
+            raise AttnError(-3, "attn_rope_apply")
+        dtype = _ROPE_DTYPES.get(x.dtype)
+        if dtype is None:
+            raise TypeError("x must be bf16, fp16 or fp32")
+        dev = torch.cuda.current_device()
+        if x.dim() != 3:
+            raise ValueError("x must be [T, H, D]")
+        T, H, _ = x.shape
+        xs = _heads_strided("x", x, H, self.D, dev)
+        if out is None:
+            out = torch.empty(T, H, self.D, dtype=x.dtype, device=x.device)
+        if out.dtype != x.dtype or out.shape != x.shape:
+            raise ValueError("out must have x's type and shape")
+        os_ = _heads_strided("out", out, H, self.D, dev)
+        pp, ps = self._pos(pos, T, dev)
+        if T == 0 or H == 0:
+            return out
+        rc = lib().attn_rope_apply(self._h, dtype, x.data_ptr(), xs, T, H, pp, ps, 1 if grad else 0, out.data_ptr(),
+                                   os_, _stream_ptr(stream))
+        _check(rc, "attn_rope_apply")
+        return out
+
+    def close(self):
+        if self._h is not None:
+            lib().attn_rope_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class Plan:
@@ -239,6 +372,183 @@ class Plan:
                                   _stream_ptr(stream))
         _check(rc, "attn_run_paged")
         return out, lse
+
+    def _paging(self, k_cache, v_cache, block_table):
+        """The cache arguments of the paged entry points, in the C ABI's order
+        (v_cache None: keys only)."""
+        i = self.info
+        shape, s = k_cache.shape, k_cache.stride()
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t is None:
+                continue
+            if t.dtype != torch.bfloat16 or t.get_device() != self.device:
+                raise TypeError(f"{name} must be a bf16 tensor of the plan's device")
+            if t.dim() != 4 or t.shape[2] != i["Hkv"] or t.shape[3] != i["D"]:
+                raise ValueError(f"{name} must be [num_pages, page_size, {i['Hkv']}, {i['D']}]")
+            if t.stride(3) != 1 or (i["Hkv"] > 1 and t.stride(2) != i["D"]):
+                raise ValueError(f"{name} must keep each token's heads contiguous")
+            if t.shape != shape or t.stride() != s:
+                raise ValueError("k_cache and v_cache must have the same shape and strides")
+        n_pages, page_size = shape[0], shape[1]
+        tok = s[1] if page_size > 1 else i["Hkv"] * i["D"]
+        bt = block_table
+        if bt.dtype != torch.int32 or bt.get_device() != self.device or bt.dim() != 2 or bt.shape[0] != i["B_max"] or \
+                (bt.shape[1] > 1 and bt.stride(1) != 1):
+            raise ValueError("block_table must be an int32 tensor [B_max, n] of the plan's device, unit column stride")
+        if bt.shape[1] * page_size < i["s_max"]:
+            raise ValueError("block_table rows must cover s_max keys")
+        return (s[0] if n_pages > 1 else page_size * tok, tok, page_size, n_pages, bt.data_ptr(),
+                bt.stride(0) if bt.shape[0] > 1 else max(bt.stride(0), bt.shape[1]))
+
+    def _per_sequence(self, name, t, n):
+        if t.dtype != torch.int32 or t.get_device() != self.device or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on the plan's device")
+        return t.data_ptr()
+
+    def _ledger(self, name, t, dtype, ld):
+        """Address of a ledger array [B_max, Hkv, ld]."""
+        i = self.info
+        if t.dtype != dtype or t.get_device() != self.device or not t.is_contiguous() or t.dim() != 3 or \
+                t.shape[0] != i["B_max"] or t.shape[1] != i["Hkv"] or t.shape[2] != ld or ld < i["s_max"]:
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor [{i['B_max']}, {i['Hkv']}, >= {i['s_max']}] "
+                             "of the plan's device (one length for the whole ledger)")
+        return t.data_ptr()
+
+    def append_paged(self, k, v, k_cache, v_cache, block_table, cu_q, cu_k, *, q=None, pos=None, rope=None,
+                     q_out=None, stream=None):
+        """q_out = plan.append_paged(k, v, k_cache, v_cache, block_table, cu_q, cu_k, *[, q, pos, rope, q_out, stream]).
+
+        Writes the new tokens' k / v [T_q, Hkv, D] (token stride free) to their
+        places in the paged cache, rotating k, and q [T_q, Hq, D] into q_out,
+        by rope at pos [n_axes, T_q] (rope None: no rotation).  cu_k counts the
+        new tokens, as run_paged takes it.  q_out may be a packed q itself; it
+        is allocated when q is given without it, and None without q.  Goes
+        through attn_append_paged."""
+        if self._h is None:
+            raise AttnError(-5, "attn_append_paged")
+        i, dev = self.info, self.device
+        T = k.shape[0]
+        if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or v.shape[0] != T:
+            raise TypeError("k and v must be bf16 tensors of the same tokens")
+        ks, vs = _heads_strided("k", k, i["Hkv"], i["D"], dev), _heads_strided("v", v, i["Hkv"], i["D"], dev)
+        qp = op = None
+        qs = 0
+        if q is not None:
+            if q.dtype != torch.bfloat16 or q.shape[0] != T:
+                raise TypeError("q must be a bf16 tensor of the same tokens as k")
+            qs = _heads_strided("q", q, i["Hq"], i["D"], dev)
+            if q_out is None:
+                q_out = torch.empty(T, i["Hq"], i["D"], dtype=torch.bfloat16, device=q.device)
+            if q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or not q_out.is_contiguous() or \
+                    q_out.get_device() != dev:
+                raise ValueError("q_out must be a contiguous bf16 tensor shaped like q, on its device")
+            qp, op = q.data_ptr(), q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        rp = pp = None
+        ps = 0
+        if rope is not None:
+            if rope.handle is None:
+                raise AttnError(-3, "attn_append_paged")
+            if pos is None:
+                raise ValueError("rope needs pos")
+            rp = rope.handle
+            pp, ps = rope._pos(pos, T, dev)
+        elif pos is not None:
+            raise ValueError("pos without rope")
+        cq, ck = self._per_sequence("cu_q", cu_q, i["B_max"] + 1), self._per_sequence("cu_k", cu_k, i["B_max"] + 1)
+        cache = self._paging(k_cache, v_cache, block_table)
+        if T:
+            rc = lib().attn_append_paged(self._h, rp, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, T, pp, ps, op,
+                                         k_cache.data_ptr(), v_cache.data_ptr(), *cache, cq, ck, _stream_ptr(stream))
+            _check(rc, "attn_append_paged")
+        return q_out
+
+    def _weights_args(self, q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream):
+        i, dev = self.info, self.device
+        if q.dtype != torch.bfloat16 or q.get_device() != dev or not q.is_contiguous():
+            raise TypeError("q must be a contiguous bf16 tensor of the plan's device")
+        if q.dim() != 3 or q.shape[1] != i["Hq"] or q.shape[2] != i["D"]:
+            raise ValueError(f"q must be [T_q, {i['Hq']}, {i['D']}]")
+        if lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or \
+                lse.dim() != 2 or lse.shape[0] != q.shape[0] or lse.shape[1] != i["Hq"]:
+            raise ValueError("lse must be a contiguous fp32 tensor [T_q, Hq] of the plan's device")
+        if (seen is None) != (born is None):
+            raise ValueError("seen and born go together")
+        first = out if out is not None else weight_in if weight_in is not None else born
+        ld = first.shape[-1] if first is not None else i["s_max"]
+        if out is None:
+            out = torch.zeros(i["B_max"], i["Hkv"], ld, dtype=torch.float32, device=q.device)
+        ledger = (self._per_sequence("cu_q", cu_q, i["B_max"] + 1), self._per_sequence("cu_k", cu_k, i["B_max"] + 1),
+                  lse.data_ptr(), decay,
+                  None if weight_in is None else self._ledger("weight_in", weight_in, torch.float32, ld),
+                  self._ledger("out", out, torch.float32, ld), ld,
+                  None if seen is None else self._per_sequence("seen", seen, i["B_max"]),
+                  None if born is None else self._ledger("born", born, torch.int32, ld), _stream_ptr(stream))
+        return out, ledger
+
+    def key_weights(self, q, k, cu_q, cu_k, lse, weight_in=None, *, decay=1.0, out=None, seen=None, born=None,
+                    stream=None):
+        """out = plan.key_weights(q, k, cu_q, cu_k, lse[, weight_in, decay, out, seen, born, stream]).
+
+        The attention weight each key is given, added to decay * weight_in
+        (both [B_max, Hkv, ld >= s_max] fp32; out may be weight_in; it is
+        allocated, zero past the sequences, when not given).  q, k, cu_q, cu_k
+        as in run(), lse its result.  With seen [B_max] and born [B_max, Hkv,
+        ld] int32, the births of the present tokens are written.  Goes through
+        attn_key_weights."""
+        if self._h is None:
+            raise AttnError(-5, "attn_key_weights")
+        i = self.info
+        if k.dtype != torch.bfloat16:
+            raise TypeError("k must be a bf16 CUDA tensor")
+        ks = _heads_strided("k", k, i["Hkv"], i["D"], self.device)
+        out, ledger = self._weights_args(q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream)
+        _check(lib().attn_key_weights(self._h, q.data_ptr(), k.data_ptr(), ks, *ledger), "attn_key_weights")
+        return out
+
+    def key_weights_paged(self, q, k_cache, block_table, cu_q, cu_k, lse, weight_in=None, *, decay=1.0, out=None,
+                          seen=None, born=None, stream=None):
+        """key_weights over a paged cache (k_cache and block_table as in
+        run_paged).  Goes through attn_key_weights_paged."""
+        if self._h is None:
+            raise AttnError(-5, "attn_key_weights_paged")
+        cache = self._paging(k_cache, None, block_table)
+        out, ledger = self._weights_args(q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream)
+        _check(lib().attn_key_weights_paged(self._h, q.data_ptr(), k_cache.data_ptr(), *cache, *ledger),
+               "attn_key_weights_paged")
+        return out
+
+    def evict_paged(self, weight, born, seen, keep, k_cache, v_cache, block_table, cu_k, *, sink=0, recent=0,
+                    weight_out=None, born_out=None, cu_k_out=None, stream=None):
+        """weight_out, born_out, cu_k_out = plan.evict_paged(weight, born, seen, keep, k_cache, v_cache, block_table,
+        cu_k, *[, sink, recent, weight_out, born_out, cu_k_out, stream]).
+
+        Cuts every sequence to min(length, keep[b]) keys in each KV head, the
+        ones of the highest weight, those born among the first `sink` or last
+        `recent` of its seen[b] tokens first; K and V rows move within the
+        cache, and the ledger (weight fp32 and born int32, [B_max, Hkv, ld])
+        with them, in place unless weight_out / born_out are given.  cu_k_out
+        [B_max + 1] gets the offsets of the new lengths.  Goes through
+        attn_evict_paged."""
+        if self._h is None:
+            raise AttnError(-5, "attn_evict_paged")
+        i = self.info
+        ld = weight.shape[-1]
+        weight_out = weight if weight_out is None else weight_out
+        born_out = born if born_out is None else born_out
+        if cu_k_out is None:
+            cu_k_out = torch.empty_like(cu_k)
+        cache = self._paging(k_cache, v_cache, block_table)
+        rc = lib().attn_evict_paged(
+            self._h, self._ledger("weight", weight, torch.float32, ld), self._ledger("born", born, torch.int32, ld),
+            self._per_sequence("seen", seen, i["B_max"]), self._per_sequence("keep", keep, i["B_max"]), int(sink),
+            int(recent), self._ledger("weight_out", weight_out, torch.float32, ld),
+            self._ledger("born_out", born_out, torch.int32, ld), ld, k_cache.data_ptr(), v_cache.data_ptr(), *cache,
+            self._per_sequence("cu_k", cu_k, i["B_max"] + 1), self._per_sequence("cu_k_out", cu_k_out, i["B_max"] + 1),
+            _stream_ptr(stream))
+        _check(rc, "attn_evict_paged")
+        return weight_out, born_out, cu_k_out
 
     def _check_common(self, q, cu_q, cu_k, out, lse, where):
         if self._h is None:

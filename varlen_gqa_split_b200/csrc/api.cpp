@@ -7,8 +7,6 @@
 // device-to-host copy, no allocation, no compilation (cudnn-frontend issue
 // #552 "frost(sdpa): THD execute host round-trip", sections Context and
 // Proposal to evaluate).
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -16,37 +14,21 @@
 #include <mutex>
 #include <unordered_set>
 
-#include "../../include/varlen_gqa.h"
 #include "kernels.h"
 #include "params.h"
-
-#define ATTN_EXPORT extern "C" __attribute__((visibility("default")))
+#include "plan.h"
 
 using namespace vgqa;
-
-struct attn_plan_s {
-    attn_plan_desc d;
-    int device;
-    int NT;                    // tensor-core path: row fragments of 8
-    float scale_log2;
-    void *scratch;             // one allocation: error word, partials
-    uint32_t *err;
-    uint32_t *ticket;          // fused-merge arrival counters
-    size_t ticket_bytes;
-    int merge_bytes;           // tensor-core path: shared bytes of the merge area
-    int qtile;                 // tensor-core path: query tokens per row tile
-    int max_rt;                // tensor-core path: row tiles per sequence at most
-    int direct;                // warp-MMA path: one block per unit, no merge
-    float *o_part;
-    float2 *ml_part;
-    unsigned long long wait_ns; // limit of one bounded wait in the kernels
-};
 
 namespace {
 
 std::mutex g_mu;
 std::unordered_set<attn_plan_s *> g_plans;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
+
+namespace vgqa {
 
 bool live(attn_plan_s *p) {
     std::lock_guard<std::mutex> lk(g_mu);
@@ -72,7 +54,7 @@ int get_encoder() {
 // so a load at row num_pages * page_rows (the kernels' stand-in for a key
 // past the sequence or a bad table entry) lies outside and fills zeros.
 int encode_kv_map(CUtensorMap *map, const void *base, int Hkv, int D, int block_n, long long token_stride,
-                  long long rows = 0x7fffffff) {
+                  long long rows) {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)token_stride * 2};
     cuuint32_t box[3] = {64, 1, (cuuint32_t)block_n};
@@ -99,6 +81,10 @@ int encode_paged_map(CUtensorMap *map, const void *base, int Hkv, int D, int pag
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_E_CUDA;
 }
+
+}  // namespace vgqa
+
+namespace {
 
 // The warp-MMA kernel's K/V maps: the same tensors with the D / 64 halves of
 // a row as the outermost dimension (stride 128 bytes), so that one box of
@@ -133,6 +119,10 @@ int encode_paged_map_halves(CUtensorMap *map, const void *base, int Hkv, int D, 
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_E_CUDA;
 }
 
+}  // namespace
+
+namespace vgqa {
+
 // [T, Hq, D] bf16, box = 64 elements x G heads x qtile tokens: one unit's
 // query rows (token-major, heads inner) as the tcgen05 kernel's A operand.
 // Loads are right-aligned to the sequence's last query token, so, as for K/V,
@@ -148,6 +138,10 @@ int encode_q_map(CUtensorMap *map, const void *base, int Hq, int D, int G, int q
     return r == CUDA_SUCCESS ? ATTN_OK : ATTN_E_CUDA;
 }
 
+}  // namespace vgqa
+
+namespace {
+
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
@@ -160,8 +154,6 @@ int share_stride(int n) {
         if (gcd(s, n) == 1) return s;
     return 1;
 }
-
-bool aligned(const void *ptr, size_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 
 }  // namespace
 
@@ -354,6 +346,8 @@ ATTN_EXPORT int attn_plan_ex(attn_plan_t *out, int B_max, int s_max, int Hq, int
         }
     }
 
+    if (evict_prepare() != cudaSuccess) return ATTN_E_CUDA;
+
     // scratch: error word, merge tickets, O partials, (m, l) partials
     const size_t off_t = 256;
     const size_t off_o = align_up(off_t + n_ticket * sizeof(uint32_t), 256);
@@ -432,20 +426,37 @@ ATTN_EXPORT int attn_plan_info(attn_plan_t plan, attn_plan_desc *desc) {
     return ATTN_OK;
 }
 
-namespace {
-
-// where the keys live when the cache is paged (attn_run_paged)
-struct Paging {
-    const int32_t *block_table;
-    int bt_stride, page_size, num_pages;
-    long long page_stride;
-};
+namespace vgqa {
 
 int log2_exact(long long x) {
     int s = 0;
     while ((1ll << s) < x) ++s;
     return (1ll << s) == x ? s : -1;
 }
+
+int check_paging(const attn_plan_s *plan, int64_t page_stride, int64_t token_stride, int page_size, int num_pages,
+                 const int32_t *block_table, int bt_stride) {
+    if (!block_table) return ATTN_E_NULL;
+    if (!aligned(block_table, 4)) return ATTN_E_ALIGNMENT;
+    const attn_plan_desc &d = plan->d;
+    const long long packed = (long long)d.Hkv * d.D;
+    // power-of-two pages of at least 8 tokens: a tile of 64 keys then covers
+    // whole pages or lies inside one, and each TMA box starts on a 1 KB
+    // boundary of the 128-byte swizzle pattern
+    const int shift = log2_exact(page_size);
+    if (page_size < 8 || page_size > (1 << 20) || shift < 0 || num_pages < 1 ||
+        (long long)num_pages * page_size >= (1ll << 31))
+        return ATTN_E_INVALID_ARG;
+    if (token_stride < packed || token_stride % 8 != 0 || token_stride > (1ll << 38) || page_stride % 8 != 0 ||
+        page_stride < (long long)page_size * token_stride || page_stride > (1ll << 38))
+        return ATTN_E_INVALID_ARG;
+    if (bt_stride < (d.s_max + page_size - 1) / page_size) return ATTN_E_INVALID_ARG;
+    return ATTN_OK;
+}
+
+}  // namespace vgqa
+
+namespace {
 
 int run_impl(attn_plan_t plan, const void *q, const void *k, const void *v, const int32_t *cu_q,
              const int32_t *cu_k, void *out, float *lse, long long k_stride, long long v_stride,
@@ -592,21 +603,8 @@ ATTN_EXPORT int attn_run_paged(attn_plan_t plan, const void *q, const void *k_ca
                                const int32_t *block_table, int bt_stride, const int32_t *cu_q,
                                const int32_t *cu_k, void *out, float *lse, void *stream) {
     if (!plan || !live(plan)) return ATTN_E_BAD_PLAN;
-    if (!block_table) return ATTN_E_NULL;
-    if (!aligned(block_table, 4)) return ATTN_E_ALIGNMENT;
-    const attn_plan_desc &d = plan->d;
-    const long long packed = (long long)d.Hkv * d.D;
-    // power-of-two pages of at least 8 tokens: a tile of 64 keys then covers
-    // whole pages or lies inside one, and each TMA box starts on a 1 KB
-    // boundary of the 128-byte swizzle pattern
-    const int shift = log2_exact(page_size);
-    if (page_size < 8 || page_size > (1 << 20) || shift < 0 || num_pages < 1 ||
-        (long long)num_pages * page_size >= (1ll << 31))
-        return ATTN_E_INVALID_ARG;
-    if (token_stride < packed || token_stride % 8 != 0 || token_stride > (1ll << 38) || page_stride % 8 != 0 ||
-        page_stride < (long long)page_size * token_stride || page_stride > (1ll << 38))
-        return ATTN_E_INVALID_ARG;
-    if (bt_stride < (d.s_max + page_size - 1) / page_size) return ATTN_E_INVALID_ARG;
+    const int rc = check_paging(plan, page_stride, token_stride, page_size, num_pages, block_table, bt_stride);
+    if (rc != ATTN_OK) return rc;
     const Paging pg{block_table, bt_stride, page_size, num_pages, page_stride};
     return run_impl(plan, q, k_cache, v_cache, cu_q, cu_k, out, lse, token_stride, token_stride, &pg, stream);
 }

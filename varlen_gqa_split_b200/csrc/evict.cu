@@ -1,0 +1,455 @@
+// evict.cu -- eviction from a paged cache by accumulated attention weight
+// (attn_evict_paged).
+//
+// For each (sequence, KV head): of its n keys the c = min(n, keep) of the
+// highest rank stay.  A key's rank is its weight, +inf for a protected key
+// (born among the first `sink` or the last `recent` tokens) and -inf for a
+// NaN; ties go to the lowest place.  Attention does not depend on the order
+// of its keys, so a kept key below c stays where it is, and the i-th kept key
+// at or above c moves into the i-th evicted place below c: no more rows move
+// than have to, and no moved row's source is another's destination, so the
+// moves need no order among themselves.
+//
+// A unit (sequence, head) is one cluster of thread blocks, each with a slice
+// of the keys:
+//   1. ranks as order-preserving 32-bit integers, kept in shared memory where
+//      the slice fits (else read again, from L2);
+//   2. the c-th largest by radix selection, 8 bits at a time: a histogram of
+//      the digit over the keys that match the prefix so far, in 8 copies to
+//      spread the collisions of alike weights, summed over the cluster's
+//      blocks through distributed shared memory;
+//   3. one bit per key, kept or not, and the counts of evicted places below c
+//      and of kept keys above, prefix-summed;
+//   4. the moves: pair i finds its place and its key by binary search in
+//      those counts, and 16 bytes a thread go from row to row.
+// The rest of the time is the latency of those steps, except for large cuts,
+// where the moved rows' bandwidth counts.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "plan.h"
+
+namespace cg = cooperative_groups;
+
+namespace vgqa {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kCopies = 8;                // histogram copies
+constexpr int kPairs = 512;               // moves located at once
+constexpr int kCoarse = 4;                // words (of 32 keys) per entry of the prefix counts
+
+struct Evict {
+    const float *w;
+    const int32_t *born, *seen, *keep;
+    float *w_out;
+    int32_t *born_out;
+    __nv_bfloat16 *k_cache, *v_cache;
+    int32_t *cu_out;
+    long long ld;
+    int sink, recent;
+    int slice_words;           // words of 32 keys a block takes of the longest sequence
+    int cached;                // keys of a slice that fit in shared memory (all or none: see smem)
+};
+
+// rank as an unsigned integer of the same order: NaN counts as -inf, -0 as +0
+__device__ __forceinline__ uint32_t order_of(float w, bool fixed) {
+    if (fixed) w = INFINITY;
+    if (w != w) w = -INFINITY;
+    const uint32_t u = __float_as_uint(w + 0.f);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// this block's sequence lengths: only cu_k counts
+__device__ __forceinline__ bool key_length(const Params &p, int b, bool report, int &Lk) {
+    const int k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+    Lk = k1 - k0;
+    const uint32_t bad = (k0 < 0 || Lk < 0) ? ATTN_DEV_ERR_OFFSETS : Lk > p.s_max ? ATTN_DEV_ERR_K_TOO_LONG : 0u;
+    if (bad && report) atomicOr(p.err, bad);
+    return bad == 0;
+}
+
+// inclusive sum over the block's threads; `scratch` [kWarps]
+__device__ __forceinline__ int block_scan(int v, int *scratch, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = v;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const int x = scratch[i];
+        if (i < warp) before += x;
+        all += x;
+    }
+    total = all;
+    return v + before;
+}
+
+// the new lengths' prefix sums
+__device__ void write_offsets(const Params &p, const Evict &e, int *scratch) {
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B_max; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int c = 0, Lk;
+        if (b < p.B_max && key_length(p, b, true, Lk)) c = min(Lk, max(0, __ldg(e.keep + b)));
+        int total;
+        const int s = block_scan(c, scratch, total);
+        if (b < p.B_max) e.cu_out[b + 1] = carry + s;
+        carry += total;
+    }
+    if (threadIdx.x == 0) e.cu_out[0] = 0;
+}
+
+// the i-th set bit (from 0) of x
+__device__ __forceinline__ int nth_bit(uint32_t x, int i) {
+    for (; i > 0; --i) x &= x - 1;
+    return __ffs(x) - 1;
+}
+
+// Shared memory: [4 digits][256] counts of this block, [256][kCopies]
+// histogram copies, scratch, then either the slice's ranks (steps 1 and 2) or,
+// from step 3 on, the whole unit's bits and prefix counts and the located
+// pairs.
+struct Head {
+    uint32_t count[4][256];
+    uint32_t hist[256 * kCopies];
+    int scratch[kWarps];
+    uint32_t digit, above, ties;          // chosen digit, keys above it, keys in it
+    int pairs[2][kPairs];                 // place, key
+};
+
+__global__ void __launch_bounds__(kThreads) evict_kernel(const Params p, const Evict e) {
+    extern __shared__ uint4 smem_raw[];
+    Head &sh = *reinterpret_cast<Head *>(smem_raw);
+    uint32_t *body = reinterpret_cast<uint32_t *>(&sh + 1);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int unit = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (unit == p.B_max * p.Hkv) {        // the extra cluster
+        if (rank == 0) write_offsets(p, e, sh.scratch);
+        return;
+    }
+    const int b = unit / p.Hkv, hk = unit % p.Hkv;
+    int n;
+    if (!key_length(p, b, false, n)) return;
+    const int c = min(n, max(0, __ldg(e.keep + b)));
+    if (c == 0) return;
+    const float *w = e.w + (long long)unit * e.ld;
+    const int32_t *born = e.born + (long long)unit * e.ld;
+    float *w_out = e.w_out + (long long)unit * e.ld;
+    int32_t *born_out = e.born_out + (long long)unit * e.ld;
+    const bool copy_w = w_out != w, copy_born = born_out != born;
+    // this block's slice, in whole words
+    const int words = (n + 31) / 32, per = (words + CS - 1) / CS;
+    const int w0 = min(words, rank * per), w1 = min(words, w0 + per);
+    const int lo = w0 * 32, hi = min(n, w1 * 32);
+    if (c == n) {                         // nothing to evict
+        for (int j = lo + tid; j < hi; j += kThreads) {
+            if (copy_w) w_out[j] = w[j];
+            if (copy_born) born_out[j] = born[j];
+        }
+        return;
+    }
+    const int last = __ldg(e.seen + b) - e.recent;
+    auto read_rank = [&](int j) -> uint32_t {
+        const int a = born[j];
+        return order_of(w[j], a < e.sink || a >= last);
+    };
+    const bool cached = e.cached >= per * 32;
+    if (cached)
+        for (int j = lo + tid; j < hi; j += kThreads) body[j - lo] = read_rank(j);
+    auto rank_of = [&](int j) -> uint32_t { return cached ? body[j - lo] : read_rank(j); };
+
+    // ---- the c-th largest rank: `prefix` after four digits; `need` of its ties stay
+    uint32_t prefix = 0;
+    int need = c, ties = 0;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        for (int i = tid; i < 256 * kCopies; i += kThreads) sh.hist[i] = 0;
+        __syncthreads();
+        for (int j = lo + tid; j < hi; j += kThreads) {
+            const uint32_t u = rank_of(j);
+            if (pass == 0 || (u >> (shift + 8)) == prefix)
+                atomicAdd(&sh.hist[((u >> shift) & 255u) * kCopies + (lane % kCopies)], 1u);
+        }
+        __syncthreads();
+        if (tid < 256) {
+            uint32_t s = 0;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) s += sh.hist[tid * kCopies + ((i + lane) % kCopies)];
+            sh.count[pass][tid] = s;
+        }
+        if (CS > 1) cluster.sync();
+        else __syncthreads();
+        // digits from the highest down: thread t takes digit 255 - t
+        int total = 0, mine = 0;
+        if (tid < 256) {
+            if (CS > 1)
+                for (int r = 0; r < CS; ++r) mine += (int)cluster.map_shared_rank(&sh.count[pass][255 - tid], r)[0];
+            else
+                mine = (int)sh.count[pass][255 - tid];
+        }
+        const int upto = block_scan(mine, sh.scratch, total);
+        if (tid < 256 && upto >= need && upto - mine < need) {
+            sh.digit = 255 - tid;
+            sh.above = upto - mine;
+            sh.ties = mine;
+        }
+        __syncthreads();
+        prefix = (prefix << 8) | sh.digit;
+        need -= (int)sh.above;
+        ties = (int)sh.ties;
+        __syncthreads();
+    }
+
+    // ---- bits: kept if above the threshold, or one of its first `need` ties.
+    // Each warp takes a contiguous run of words; ties before it are counted
+    // first where not all of them stay.
+    const int wpw = (w1 - w0 + kWarps - 1) / kWarps;
+    const int ww0 = min(w1, w0 + warp * wpw), ww1 = min(w1, ww0 + wpw);
+    int tie_at = 0;
+    if (ties != need) {
+        int t = 0;
+        for (int wd = ww0; wd < ww1; ++wd) {
+            const int j = wd * 32 + lane;
+            t += __popc(__ballot_sync(0xffffffffu, j < hi && rank_of(j) == prefix));
+        }
+        __syncthreads();
+        if (lane == 0) sh.scratch[warp] = t;
+        __syncthreads();
+        for (int i = 0; i < warp; ++i) tie_at += sh.scratch[i];
+        // lower ranks' ties: their counts of the last digit
+        for (int r = 0; r < rank; ++r) tie_at += (int)cluster.map_shared_rank(&sh.count[3][prefix & 255u], r)[0];
+    }
+    // the unit's bits go behind the ranks (other blocks still need theirs)
+    uint32_t *bits = body + (cached ? e.cached : 0);
+    uint32_t *pre = bits + e.slice_words * CS;          // [slice_words CS / kCoarse + 1] evicted below c, kept above
+    for (int wd = ww0; wd < ww1; ++wd) {
+        const int j = wd * 32 + lane;
+        const uint32_t u = j < hi ? rank_of(j) : 0u;
+        const uint32_t above = __ballot_sync(0xffffffffu, j < hi && u > prefix);
+        const uint32_t tie = __ballot_sync(0xffffffffu, j < hi && u == prefix);
+        const bool in = (above >> lane & 1u) ||
+                        ((tie >> lane & 1u) && tie_at + __popc(tie & ((1u << lane) - 1u)) < need);
+        const uint32_t kept = __ballot_sync(0xffffffffu, in);
+        tie_at += __popc(tie);
+        // the bit of interest: evicted where j < c, kept where j >= c
+        const uint32_t below = c - wd * 32 >= 32 ? 0xffffffffu : c > wd * 32 ? (1u << (c - wd * 32)) - 1u : 0u;
+        if (lane == 0) bits[wd] = kept ^ below;
+        if (in && j < c) {                              // stays where it is
+            if (copy_w) w_out[j] = w[j];
+            if (copy_born) born_out[j] = born[j];
+        }
+    }
+    // ---- every block gets the whole unit's bits
+    if (CS > 1) {
+        cluster.sync();
+        for (int r = 0; r < CS; ++r) {
+            if (r == rank) continue;
+            const uint32_t *src = cluster.map_shared_rank(bits, r);
+            const int a0 = min(words, r * per), a1 = min(words, a0 + per);
+            for (int i = a0 + tid; i < a1; i += kThreads) bits[i] = src[i];
+        }
+        cluster.sync();                                 // also: nobody leaves while others read its memory
+    } else {
+        __syncthreads();
+    }
+    // prefix counts of the interesting bits at every kCoarse words: evicted
+    // places first, then, from the word of c on, kept keys.  The word that
+    // holds c has both; its low bits belong to the places.
+    const int coarse = (words + kCoarse - 1) / kCoarse;
+    int carry = 0;
+    for (int i0 = 0; i0 < coarse; i0 += kThreads) {
+        const int i = i0 + tid;
+        int s = 0;
+        if (i < coarse)
+            for (int k = 0; k < kCoarse; ++k)
+                if (i * kCoarse + k < words) s += __popc(bits[i * kCoarse + k]);
+        int total;
+        const int inc = block_scan(s, sh.scratch, total);
+        if (i < coarse) pre[i] = carry + inc - s;
+        carry += total;
+    }
+    __syncthreads();
+    // the bits in order: the m evicted places below c, then the m kept keys
+    const int m = carry / 2;
+    auto locate = [&](int i) -> int {                   // the place of the i-th bit
+        int a = 0, z = coarse;                          // pre[a] <= i < pre[z]
+        while (z - a > 1) {
+            const int mid = (a + z) >> 1;
+            if ((int)pre[mid] <= i) a = mid;
+            else z = mid;
+        }
+        int left = i - (int)pre[a], wd = a * kCoarse;
+        for (;; ++wd) {
+            const int k = __popc(bits[wd]);
+            if (left < k) break;
+            left -= k;
+        }
+        return wd * 32 + nth_bit(bits[wd], left);
+    };
+
+    // ---- moves, an equal share of the pairs for each block
+    const int m0 = (int)((long long)m * rank / CS), m1 = (int)((long long)m * (rank + 1) / CS);
+    const int vecs = p.D / 8;                           // 16-byte pieces of a row
+    const int slot_mask = (1 << p.page_shift) - 1;
+    for (int i0 = m0; i0 < m1; i0 += kPairs) {
+        const int np = min(kPairs, m1 - i0);
+        __syncthreads();
+        for (int i = tid; i < np; i += kThreads) {
+            const int to = locate(i0 + i), at = locate(m + i0 + i);
+            w_out[to] = w[at];
+            born_out[to] = born[at];
+            const int pt = page_of(p, b, to), pa = page_of(p, b, at);
+            const bool ok = pt < p.num_pages && pa < p.num_pages;
+            sh.pairs[0][i] = ok ? (pt << p.page_shift) | (to & slot_mask) : -1;
+            sh.pairs[1][i] = ok ? (pa << p.page_shift) | (at & slot_mask) : -1;
+        }
+        __syncthreads();
+        constexpr int kUnroll = 4;
+        const int items = np * 2 * vecs;
+        for (int x0 = tid; x0 < items; x0 += kUnroll * kThreads) {
+            uint4 val[kUnroll];
+            uint4 *dst[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int x = x0 + u * kThreads;
+                dst[u] = nullptr;
+                if (x < items) {
+                    const int i = x / (2 * vecs), r = x % (2 * vecs);
+                    const int to = sh.pairs[0][i], at = sh.pairs[1][i];
+                    if (to >= 0) {
+                        __nv_bfloat16 *cache = r < vecs ? e.k_cache : e.v_cache;
+                        const long long in_row = (long long)hk * p.D + (r % vecs) * 8;
+                        dst[u] = reinterpret_cast<uint4 *>(cache + (long long)(to >> p.page_shift) * p.page_stride +
+                                                           (long long)(to & slot_mask) * p.k_stride + in_row);
+                        val[u] = *reinterpret_cast<const uint4 *>(
+                            cache + (long long)(at >> p.page_shift) * p.page_stride +
+                            (long long)(at & slot_mask) * p.k_stride + in_row);
+                    }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (dst[u]) *dst[u] = val[u];
+        }
+    }
+}
+
+constexpr int kMaxSmem = 200 * 1024;
+constexpr int kMaxKeys = 1 << 20;         // bits and counts of 2^20 keys take 160 KB
+
+// words of a slice, and shared memory, for clusters of `cs` blocks
+int slice_words(int s_max, int cs) { return ((s_max + 31) / 32 + cs - 1) / cs; }
+size_t bits_bytes(int s_max, int cs) {
+    const size_t words = (size_t)slice_words(s_max, cs) * cs;
+    return words * 4 + (words / kCoarse + 2) * 4;
+}
+
+}  // namespace
+
+cudaError_t evict_prepare() {
+    return cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+}
+
+namespace {
+
+cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
+    const int cs = 1;
+    e.slice_words = slice_words(p.s_max, cs);
+    const size_t fixed = sizeof(Head) + bits_bytes(p.s_max, cs), ranks = (size_t)e.slice_words * 32 * 4;
+    e.cached = fixed + ranks <= (size_t)kMaxSmem ? e.slice_words * 32 : 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((p.B_max * p.Hkv + 1) * cs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = fixed + (e.cached ? ranks : 0);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_kernel, p, e);
+}
+
+bool overlap(const void *a, const void *b, size_t na, size_t nb) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+}  // namespace vgqa
+
+using namespace vgqa;
+
+ATTN_EXPORT int attn_evict_paged(attn_plan_t plan, const float *weight, const int32_t *born, const int32_t *seen,
+                                 const int32_t *keep, int sink, int recent, float *weight_out, int32_t *born_out,
+                                 int64_t ld, void *k_cache, void *v_cache, int64_t page_stride, int64_t token_stride,
+                                 int page_size, int num_pages, const int32_t *block_table, int bt_stride,
+                                 const int32_t *cu_k, int32_t *cu_k_out, void *stream) {
+    if (!plan || !live(plan)) return ATTN_E_BAD_PLAN;
+    if (!weight || !born || !seen || !keep || !weight_out || !born_out || !k_cache || !v_cache || !cu_k || !cu_k_out)
+        return ATTN_E_NULL;
+    const int rc = check_paging(plan, page_stride, token_stride, page_size, num_pages, block_table, bt_stride);
+    if (rc != ATTN_OK) return rc;
+    const attn_plan_desc &d = plan->d;
+    if (d.s_max > kMaxKeys) return ATTN_E_UNSUPPORTED;
+    if (sink < 0 || recent < 0 || ld < d.s_max || ld > (1ll << 38)) return ATTN_E_INVALID_ARG;
+    if ((long long)d.B_max * d.Hkv >= (1ll << 27)) return ATTN_E_UNSUPPORTED;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return ATTN_E_ALIGNMENT;
+    for (const void *ptr : {(const void *)weight, (const void *)born, (const void *)seen, (const void *)keep,
+                            (const void *)weight_out, (const void *)born_out, (const void *)cu_k,
+                            (const void *)cu_k_out})
+        if (!aligned(ptr, 4)) return ATTN_E_ALIGNMENT;
+    // in place, or apart
+    const size_t led = (size_t)d.B_max * d.Hkv * ld * 4, cu = ((size_t)d.B_max + 1) * 4;
+    if ((weight_out != weight && overlap(weight, weight_out, led, led)) ||
+        (born_out != born && overlap(born, born_out, led, led)) || overlap(weight_out, born_out, led, led) ||
+        overlap(weight_out, born, led, led) || overlap(born_out, weight, led, led) ||
+        overlap(cu_k, cu_k_out, cu, cu) || overlap(keep, cu_k_out, cu - 4, cu))
+        return ATTN_E_INVALID_ARG;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_E_CUDA;
+    if (dev != plan->device) return ATTN_E_DEVICE;
+    Params p{};
+    p.cu_k = cu_k;
+    p.err = plan->err;
+    p.B_max = d.B_max;
+    p.s_max = d.s_max;
+    p.Hkv = d.Hkv;
+    p.D = d.D;
+    p.k_stride = token_stride;
+    p.block_table = block_table;
+    p.bt_stride = bt_stride;
+    p.page_shift = log2_exact(page_size);
+    p.num_pages = num_pages;
+    p.page_stride = page_stride;
+    Evict e{};
+    e.w = weight;
+    e.born = born;
+    e.seen = seen;
+    e.keep = keep;
+    e.w_out = weight_out;
+    e.born_out = born_out;
+    e.k_cache = static_cast<__nv_bfloat16 *>(k_cache);
+    e.v_cache = static_cast<__nv_bfloat16 *>(v_cache);
+    e.cu_out = cu_k_out;
+    e.ld = ld;
+    e.sink = sink;
+    e.recent = recent;
+    return launch_evict(p, e, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_E_CUDA;
+}

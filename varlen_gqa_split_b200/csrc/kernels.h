@@ -51,4 +51,11 @@ cudaError_t launch_combine_slots(const Params &p, int ctas, cudaStream_t stream)
 int combine_blocks(const Params &p);
 cudaError_t launch_combine(const Params &p, cudaStream_t stream);
 
+// accumulated attention weights on the CUDA cores (any row count)
+struct KeyWeights;
+cudaError_t launch_key_weights_simt(const Params &p, const KeyWeights &kw, cudaStream_t stream);
+
+// eviction: opt in to its shared memory (once per plan, outside capture)
+cudaError_t evict_prepare();
+
 }  // namespace vgqa

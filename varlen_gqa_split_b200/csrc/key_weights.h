@@ -1,0 +1,19 @@
+// key_weights.h -- what the accumulated-attention-weight kernels share
+// (internal).
+#pragma once
+
+#include "params.h"
+
+namespace vgqa {
+
+// Besides the plan's Params (lse is an input here and out unused):
+struct KeyWeights {
+    const float *w_in;         // [B_max, Hkv, ld], or NULL: start from zero
+    float *w_out;              // [B_max, Hkv, ld]
+    const int32_t *seen;       // [B_max] or NULL
+    int32_t *born;             // [B_max, Hkv, ld] or NULL
+    long long ld;
+    float decay;
+};
+
+}  // namespace vgqa

@@ -1,0 +1,90 @@
+// rope.cuh -- rotary positions with several axes: the table, the angle and
+// the rotation of one group of pairs (device code and host struct, internal).
+//
+// Pair i of a head turns by theta = pos[axis_i] * f_i:
+//     (u, w) -> scale (u cos theta - w sin theta, u sin theta + w cos theta).
+// The angle is kept in turns as a 64-bit fixed-point fraction: with
+// F_i = round(f_i / 2 pi * 2^64) mod 2^64, the product pos * F_i mod 2^64 is
+// the exact fraction of a turn for the rounded F_i, since whole turns wrap
+// away by themselves.  |pos| < 2^31 makes its error at most 2^-34 turns
+// (4e-10 rad) at any distance; an angle in 32-bit floating point would be off
+// by 0.06 rad at position 2^20.  The fraction's upper 32 bits then go to
+// sincospif, whose argument in half turns has 24 significant bits: an error
+// of at most pi 2^-25 = 9.4e-8 rad, below the rounding of cos and sin to fp32
+// near one and far below that of the 16-bit types.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace vgqa {
+
+constexpr int kRopeMaxPairs = 128;        // head sizes up to 256
+constexpr int kRopeMaxAxes = 8;
+
+// passed to the kernels by value (1.2 KB of parameters): a rotation needs no
+// device memory of its own and serves any device
+struct RopeTable {
+    unsigned long long turn[kRopeMaxPairs];   // F_i
+    uint8_t axis[kRopeMaxPairs];
+    int n;                                    // pairs; elements [2 n, D) are copied
+    float scale;
+};
+
+// (scale cos, scale sin) of pair i at `pos` positions; sign -1 turns backwards
+__device__ __forceinline__ float2 rope_cos_sin(const RopeTable &tab, int i, int pos, float sign) {
+    const unsigned long long t = (unsigned long long)(long long)pos * tab.turn[i];
+    const int hi = (int)((t + 0x80000000ull) >> 32);          // 2^-32 turns, in [-1/2, 1/2) turn
+    float s, c;
+    sincospif((float)hi * 4.656612873077393e-10f, &s, &c);    // half turns: hi * 2^-31
+    return make_float2(c * tab.scale, s * tab.scale * sign);
+}
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// V elements moved by one access
+template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T e[V]; };
+
+// The elements of group g of a head: 2 V of them in two accesses of V.  The
+// first n / V groups hold V pairs each ("half": elements g V .. and n + g V
+// ..; "interleaved": 2 g V .. and the next V), the others the D - 2 n copied
+// elements, of which the last group may hold V only.
+template <int V, bool HALF>
+__device__ __forceinline__ void rope_offsets(int g, int n, int D, int &a, int &b) {
+    if (g * V < n) {
+        a = HALF ? g * V : 2 * g * V;
+        b = HALF ? n + g * V : a + V;
+    } else {
+        a = 2 * n + (g - n / V) * 2 * V;
+        b = a + V < D ? a + V : -1;
+    }
+}
+__host__ __device__ __forceinline__ int rope_groups(int n, int D, int V) {
+    return n / V + (D - 2 * n + 2 * V - 1) / (2 * V);
+}
+
+// rotate the V pairs held in (x, y) by the factors cs[0 .. V)
+template <typename T, int V, bool HALF>
+__device__ __forceinline__ void rope_rotate(Vec<T, V> &x, Vec<T, V> &y, const float2 *cs) {
+    T *p[2] = {x.e, y.e};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        // the pair's two elements: i of x and i of y, or 2 i and 2 i + 1 of x then y
+        T &u = HALF ? p[0][i] : p[(2 * i) / V][(2 * i) % V];
+        T &w = HALF ? p[1][i] : p[(2 * i + 1) / V][(2 * i + 1) % V];
+        const float2 c = cs[i];
+        const float fu = to_f32(u), fw = to_f32(w);
+        u = from_f32<T>(fu * c.x - fw * c.y);
+        w = from_f32<T>(fu * c.y + fw * c.x);
+    }
+}
+
+}  // namespace vgqa
