@@ -348,11 +348,31 @@ ATTN_EXPORT int attn_plan_ex(attn_plan_t *out, int B_max, int s_max, int Hq, int
 
     if (evict_prepare() != cudaSuccess) return ATTN_E_CUDA;
 
-    // scratch: error word, merge tickets, O partials, (m, l) partials
+    // accumulated attention weights: the tensor-core path wherever one token's
+    // G heads fit a row tile of 128; blocks that may share an item of keys
+    // (several row tiles) get room for their parts of its sums
+    int kw_columns = 0, kw_qtile = 0, kw_ctas = 0;
+    size_t kw_part = 0;
+    const size_t kw_ticket_at = n_ticket;
+    if (G_ <= tc_rows()) {
+        kw_qtile = std::min(max_q, tc_rows() / G_);
+        kw_columns = key_weights_columns(G_ * kw_qtile);
+        const int kw_rt = (max_q + kw_qtile - 1) / kw_qtile;
+        kw_ctas = (int)std::min<long long>(sms, (long long)B_max * Hkv * ((s_max + 255) / 256) * kw_rt);
+        if (kw_rt > 1) {
+            kw_part = (size_t)kw_ctas * key_weights_part_floats();
+            n_ticket += (size_t)kw_ctas * key_weights_tickets();
+        }
+        if (key_weights_tc_prepare(D, kw_columns) != cudaSuccess) return ATTN_E_CUDA;
+    }
+
+    // scratch: error word, merge tickets, O partials, (m, l) partials, parts
+    // of key weights
     const size_t off_t = 256;
     const size_t off_o = align_up(off_t + n_ticket * sizeof(uint32_t), 256);
     const size_t off_ml = align_up(off_o + n_part * part_rows * D * sizeof(float), 256);
-    const size_t total = align_up(off_ml + n_part * part_rows * sizeof(float2), 256);
+    const size_t off_kw = align_up(off_ml + n_part * part_rows * sizeof(float2), 256);
+    const size_t total = align_up(off_kw + kw_part * sizeof(float), 256);
     d.scratch_bytes = total;
 
     attn_plan_s *p = new (std::nothrow) attn_plan_s{};
@@ -376,6 +396,11 @@ ATTN_EXPORT int attn_plan_ex(attn_plan_t *out, int B_max, int s_max, int Hq, int
     p->ticket_bytes = n_ticket * sizeof(uint32_t);
     p->o_part = n_part ? reinterpret_cast<float *>(static_cast<char *>(p->scratch) + off_o) : nullptr;
     p->ml_part = n_part ? reinterpret_cast<float2 *>(static_cast<char *>(p->scratch) + off_ml) : nullptr;
+    p->kw_columns = kw_columns;
+    p->kw_qtile = kw_qtile;
+    p->kw_ctas = kw_ctas;
+    p->kw_part = kw_part ? reinterpret_cast<float *>(static_cast<char *>(p->scratch) + off_kw) : nullptr;
+    p->kw_ticket = kw_part ? p->ticket + kw_ticket_at : nullptr;
     // error word, then the test hook's stall count (parts that never arrive,
     // cleared by attn_check_error), then the merge counters
     const uint32_t stall = o ? (uint32_t)o->test_stall : 0u;
@@ -390,7 +415,7 @@ ATTN_EXPORT int attn_plan_ex(attn_plan_t *out, int B_max, int s_max, int Hq, int
         std::lock_guard<std::mutex> lk(g_mu);
         g_plans.insert(p);
     }
-    if (variant == ATTN_VARIANT_MMA || variant == ATTN_VARIANT_TC) {
+    if (variant == ATTN_VARIANT_MMA || variant == ATTN_VARIANT_TC || kw_columns) {
         int rc = get_encoder();
         if (rc != ATTN_OK) {
             attn_destroy(p);

@@ -55,6 +55,15 @@ cudaError_t launch_combine(const Params &p, cudaStream_t stream);
 struct KeyWeights;
 cudaError_t launch_key_weights_simt(const Params &p, const KeyWeights &kw, cudaStream_t stream);
 
+// ... and on the tensor cores: rows (G heads x query tokens) in tiles of up
+// to 128, `columns` wide
+int key_weights_columns(int rows);
+int key_weights_part_floats();             // per block, for cut items: floats of scratch
+int key_weights_tickets();                 // and counters
+cudaError_t key_weights_tc_prepare(int D, int columns);
+cudaError_t launch_key_weights_tc(const Params &p, const KeyWeights &kw, const CUtensorMap &tm_q,
+                                  const CUtensorMap &tm_k, int columns, int ctas, cudaStream_t stream);
+
 // eviction: opt in to its shared memory (once per plan, outside capture)
 cudaError_t evict_prepare();
 

@@ -58,8 +58,27 @@ int key_weights(attn_plan_t plan, const void *q, const void *k, long long k_stri
         p.page_box = pg->page_size < 64 ? pg->page_size : 64;
         p.page_stride = pg->page_stride;
     }
-    KeyWeights kw{weight_in, weight_out, seen, born, ld, decay};
-    const cudaError_t e = launch_key_weights_simt(p, kw, static_cast<cudaStream_t>(stream));
+    KeyWeights kw{weight_in, weight_out, seen, born, ld, decay, plan->kw_part, plan->kw_ticket};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!plan->kw_columns) return launch_key_weights_simt(p, kw, s) == cudaSuccess ? ATTN_OK : ATTN_E_CUDA;
+
+    p.qtile = plan->kw_qtile;
+    CUtensorMap tm_q, tm_k;
+    int rc = encode_q_map(&tm_q, q, d.Hq, d.D, d.G, p.qtile);
+    if (rc != ATTN_OK) return rc;
+    if (pg) {
+        // pages a whole number of token rows apart: one row index per key
+        if (pg->page_stride % k_stride == 0 && (long long)pg->num_pages * (pg->page_stride / k_stride) < (1ll << 31))
+            p.page_rows = (int)(pg->page_stride / k_stride);
+        rc = p.page_rows ? encode_kv_map(&tm_k, k, d.Hkv, d.D, p.page_box, k_stride,
+                                         (long long)pg->num_pages * p.page_rows)
+                         : encode_paged_map(&tm_k, k, d.Hkv, d.D, pg->page_size, pg->num_pages, k_stride,
+                                            pg->page_stride);
+    } else {
+        rc = encode_kv_map(&tm_k, k, d.Hkv, d.D, 128, k_stride);
+    }
+    if (rc != ATTN_OK) return rc;
+    const cudaError_t e = launch_key_weights_tc(p, kw, tm_q, tm_k, plan->kw_columns, plan->kw_ctas, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_E_CUDA;
 }
 

@@ -14,6 +14,9 @@ struct KeyWeights {
     int32_t *born;             // [B_max, Hkv, ld] or NULL
     long long ld;
     float decay;
+    float *part;               // tensor-core path: two parts of 256 sums per block, for items cut
+                               // between blocks (NULL where one row tile holds all rows: no cuts)
+    uint32_t *ticket;          // and counts of finished parts, one per block and epilogue warp
 };
 
 }  // namespace vgqa

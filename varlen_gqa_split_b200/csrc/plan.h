@@ -25,6 +25,11 @@ struct attn_plan_s {
     int direct;                // warp-MMA path: one block per unit, no merge
     float *o_part;
     float2 *ml_part;
+    int kw_columns;            // attn_key_weights: columns of a row tile; 0: CUDA cores (G > 128)
+    int kw_qtile;              // its query tokens per row tile
+    int kw_ctas;               // its blocks
+    float *kw_part;            // its scratch for items cut between blocks
+    uint32_t *kw_ticket;
     unsigned long long wait_ns; // limit of one bounded wait in the kernels
 };
 
