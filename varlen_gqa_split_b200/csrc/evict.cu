@@ -15,9 +15,9 @@
 //   1. ranks as order-preserving 32-bit integers, kept in shared memory where
 //      the slice fits (else read again, from L2);
 //   2. the c-th largest by radix selection, 8 bits at a time: a histogram of
-//      the digit over the keys that match the prefix so far, in 8 copies to
+//      the digit over the keys that match the prefix so far, in copies to
 //      spread the collisions of alike weights, summed over the cluster's
-//      blocks through distributed shared memory;
+//      blocks through distributed shared memory.  It ends early once all keys of the digit stay;
 //   3. one bit per key, kept or not, and the counts of evicted places below c
 //      and of kept keys above, prefix-summed;
 //   4. the moves: pair i finds its place and its key by binary search in
@@ -38,10 +38,12 @@ namespace vgqa {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
+constexpr int kBlocksPerSm = 4;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCopies = 8;                // histogram copies
-constexpr int kPairs = 512;               // moves located at once
+constexpr int kCopies = 4;                // histogram copies
+constexpr int kBatch = 8;                 // loads of a thread in flight
+constexpr int kMaxCluster = 8;
 constexpr int kCoarse = 4;                // words (of 32 keys) per entry of the prefix counts
 
 struct Evict {
@@ -111,25 +113,48 @@ __device__ void write_offsets(const Params &p, const Evict &e, int *scratch) {
     if (threadIdx.x == 0) e.cu_out[0] = 0;
 }
 
-// the i-th set bit (from 0) of x
-__device__ __forceinline__ int nth_bit(uint32_t x, int i) {
-    for (; i > 0; --i) x &= x - 1;
-    return __ffs(x) - 1;
+// the place of the i-th set bit (from 0) of the kCoarse words from entry a on
+__device__ __forceinline__ int pick(const uint32_t *bits, int a, int i, int words) {
+    uint32_t x[kCoarse];
+#pragma unroll
+    for (int k = 0; k < kCoarse; ++k) x[k] = a * kCoarse + k < words ? bits[a * kCoarse + k] : 0u;
+    int at = a * kCoarse * 32;
+    uint32_t w = x[0];
+    bool past = true;
+#pragma unroll
+    for (int k = 0; k + 1 < kCoarse; ++k) {
+        const int n = __popc(x[k]);
+        past = past && i >= n;
+        if (past) {
+            i -= n;
+            at += 32;
+            w = x[k + 1];
+        }
+    }
+    // halve the word: is the bit in the lower part?
+#pragma unroll
+    for (int h = 16; h; h >>= 1) {
+        const int n = __popc(w & ((1u << h) - 1u));
+        if (i >= n) {
+            i -= n;
+            at += h;
+            w >>= h;
+        }
+    }
+    return at;
 }
 
-// Shared memory: [4 digits][256] counts of this block, [256][kCopies]
-// histogram copies, scratch, then either the slice's ranks (steps 1 and 2) or,
-// from step 3 on, the whole unit's bits and prefix counts and the located
-// pairs.
+// Shared memory: this, then either the slice's ranks (steps 1 and 2) or, from
+// step 3 on and behind them, the whole unit's bits and prefix counts.
 struct Head {
-    uint32_t count[4][256];
-    uint32_t hist[256 * kCopies];
+    uint32_t hist[2][256 * kCopies];
+    uint32_t count[4][256];               // each pass's digit counts of this block (read by the cluster)
+    uint32_t total[256];                  // and of the cluster
+    int found[3];                         // the digit, the keys above it, the keys of it
     int scratch[kWarps];
-    uint32_t digit, above, ties;          // chosen digit, keys above it, keys in it
-    int pairs[2][kPairs];                 // place, key
 };
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const Params p, const Evict e) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Params p, const Evict e) {
     extern __shared__ uint4 smem_raw[];
     Head &sh = *reinterpret_cast<Head *>(smem_raw);
     uint32_t *body = reinterpret_cast<uint32_t *>(&sh + 1);
@@ -141,9 +166,10 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Params p, const E
         return;
     }
     const int b = unit / p.Hkv, hk = unit % p.Hkv;
+    const int keep = __ldg(e.keep + b), seen = __ldg(e.seen + b);   // on their way with the length
     int n;
     if (!key_length(p, b, false, n)) return;
-    const int c = min(n, max(0, __ldg(e.keep + b)));
+    const int c = min(n, max(0, keep));
     if (c == 0) return;
     const float *w = e.w + (long long)unit * e.ld;
     const int32_t *born = e.born + (long long)unit * e.ld;
@@ -161,56 +187,100 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Params p, const E
         }
         return;
     }
-    const int last = __ldg(e.seen + b) - e.recent;
+    const int last = seen - e.recent;
     auto read_rank = [&](int j) -> uint32_t {
-        const int a = born[j];
-        return order_of(w[j], a < e.sink || a >= last);
+        const int a = __ldcg(born + j);
+        return order_of(__ldcg(w + j), a < e.sink || a >= last);
     };
     const bool cached = e.cached >= per * 32;
-    if (cached)
-        for (int j = lo + tid; j < hi; j += kThreads) body[j - lo] = read_rank(j);
+    for (int i = tid; i < 256 * kCopies; i += kThreads) sh.hist[0][i] = 0;
+    // one pass over the ledger: ranks into shared memory, entries below c to
+    // the result (those of evicted keys are written again by the moves)
+    if (cached || copy_w || copy_born)
+        for (int j0 = lo + tid; j0 < hi; j0 += kBatch * kThreads) {
+            float x[kBatch];
+            int a[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int j = j0 + i * kThreads;
+                x[i] = j < hi ? __ldcg(w + j) : 0.f;
+                a[i] = j < hi ? __ldcg(born + j) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int j = j0 + i * kThreads;
+                if (j < hi && cached) body[j - lo] = order_of(x[i], a[i] < e.sink || a[i] >= last);
+                if (j < min(hi, c)) {
+                    if (copy_w) w_out[j] = x[i];
+                    if (copy_born) born_out[j] = a[i];
+                }
+            }
+        }
     auto rank_of = [&](int j) -> uint32_t { return cached ? body[j - lo] : read_rank(j); };
+    __syncthreads();
 
-    // ---- the c-th largest rank: `prefix` after four digits; `need` of its ties stay
+    // ---- the c-th largest rank: after the passes, the ranks above it are those
+    // with rank >> shift above `prefix`, and `need` of the `ties` equal to it stay
     uint32_t prefix = 0;
-    int need = c, ties = 0;
-    for (int pass = 0; pass < 4; ++pass) {
-        const int shift = 24 - 8 * pass;
-        for (int i = tid; i < 256 * kCopies; i += kThreads) sh.hist[i] = 0;
-        __syncthreads();
+    int need = c, ties = n, shift = 32;
+    for (int pass = 0; pass < 4 && ties != need; ++pass) {
+        shift -= 8;
+        uint32_t *hist = sh.hist[pass & 1];
         for (int j = lo + tid; j < hi; j += kThreads) {
             const uint32_t u = rank_of(j);
             if (pass == 0 || (u >> (shift + 8)) == prefix)
-                atomicAdd(&sh.hist[((u >> shift) & 255u) * kCopies + (lane % kCopies)], 1u);
+                atomicAdd(&hist[((u >> shift) & 255u) * kCopies + (lane % kCopies)], 1u);
         }
         __syncthreads();
-        if (tid < 256) {
-            uint32_t s = 0;
+        uint32_t mine = 0;
 #pragma unroll
-            for (int i = 0; i < kCopies; ++i) s += sh.hist[tid * kCopies + ((i + lane) % kCopies)];
-            sh.count[pass][tid] = s;
+        for (int i = 0; i < kCopies; ++i) mine += hist[tid * kCopies + ((i + lane) % kCopies)];
+        sh.count[pass][tid] = mine;
+        for (int i = tid; i < 256 * kCopies; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;
+        if (CS > 1) {
+            cluster.sync();
+            mine = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < CS) mine += *cluster.map_shared_rank(&sh.count[pass][tid], r);
         }
-        if (CS > 1) cluster.sync();
-        else __syncthreads();
-        // digits from the highest down: thread t takes digit 255 - t
-        int total = 0, mine = 0;
-        if (tid < 256) {
-            if (CS > 1)
-                for (int r = 0; r < CS; ++r) mine += (int)cluster.map_shared_rank(&sh.count[pass][255 - tid], r)[0];
-            else
-                mine = (int)sh.count[pass][255 - tid];
-        }
-        const int upto = block_scan(mine, sh.scratch, total);
-        if (tid < 256 && upto >= need && upto - mine < need) {
-            sh.digit = 255 - tid;
-            sh.above = upto - mine;
-            sh.ties = mine;
+        sh.total[tid] = mine;
+        __syncthreads();
+        if (warp == 0) {
+            // lane l: digits 255 - 8 l down to 248 - 8 l
+            uint32_t d[8];
+            *reinterpret_cast<uint4 *>(d) = *reinterpret_cast<const uint4 *>(sh.total + 248 - 8 * lane);
+            *reinterpret_cast<uint4 *>(d + 4) = *reinterpret_cast<const uint4 *>(sh.total + 252 - 8 * lane);
+            int sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += (int)d[i];
+            int upto = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += x;
+            }
+            int above = upto - sum;
+            if (above < need && upto >= need) {         // one lane holds the digit
+                bool open = true;
+#pragma unroll
+                for (int i = 7; i >= 0; --i)
+                    if (open) {
+                        if (above + (int)d[i] >= need) {
+                            sh.found[0] = 248 - 8 * lane + i;
+                            sh.found[1] = above;
+                            sh.found[2] = (int)d[i];
+                            open = false;
+                        } else {
+                            above += (int)d[i];
+                        }
+                    }
+            }
         }
         __syncthreads();
-        prefix = (prefix << 8) | sh.digit;
-        need -= (int)sh.above;
-        ties = (int)sh.ties;
-        __syncthreads();
+        prefix = (prefix << 8) | (uint32_t)sh.found[0];
+        need -= sh.found[1];
+        ties = sh.found[2];
     }
 
     // ---- bits: kept if above the threshold, or one of its first `need` ties.
@@ -223,7 +293,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Params p, const E
         int t = 0;
         for (int wd = ww0; wd < ww1; ++wd) {
             const int j = wd * 32 + lane;
-            t += __popc(__ballot_sync(0xffffffffu, j < hi && rank_of(j) == prefix));
+            t += __popc(__ballot_sync(0xffffffffu, j < hi && rank_of(j) == prefix));   // shift is 0 here
         }
         __syncthreads();
         if (lane == 0) sh.scratch[warp] = t;
@@ -237,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Params p, const E
     uint32_t *pre = bits + e.slice_words * CS;          // [slice_words CS / kCoarse + 1] evicted below c, kept above
     for (int wd = ww0; wd < ww1; ++wd) {
         const int j = wd * 32 + lane;
-        const uint32_t u = j < hi ? rank_of(j) : 0u;
+        const uint32_t u = j < hi ? rank_of(j) >> shift : 0u;
         const uint32_t above = __ballot_sync(0xffffffffu, j < hi && u > prefix);
         const uint32_t tie = __ballot_sync(0xffffffffu, j < hi && u == prefix);
         const bool in = (above >> lane & 1u) ||
@@ -247,10 +317,6 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Params p, const E
         // the bit of interest: evicted where j < c, kept where j >= c
         const uint32_t below = c - wd * 32 >= 32 ? 0xffffffffu : c > wd * 32 ? (1u << (c - wd * 32)) - 1u : 0u;
         if (lane == 0) bits[wd] = kept ^ below;
-        if (in && j < c) {                              // stays where it is
-            if (copy_w) w_out[j] = w[j];
-            if (copy_born) born_out[j] = born[j];
-        }
     }
     // ---- every block gets the whole unit's bits
     if (CS > 1) {
@@ -282,67 +348,64 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const Params p, const E
         carry += total;
     }
     __syncthreads();
-    // the bits in order: the m evicted places below c, then the m kept keys
+    // the bits in order: the m evicted places below c, then the m kept keys that
+    // take them
     const int m = carry / 2;
-    auto locate = [&](int i) -> int {                   // the place of the i-th bit
-        int a = 0, z = coarse;                          // pre[a] <= i < pre[z]
-        while (z - a > 1) {
-            const int mid = (a + z) >> 1;
-            if ((int)pre[mid] <= i) a = mid;
-            else z = mid;
+    // the places of the i-th and the k-th bit, searched for side by side
+    auto locate = [&](int i, int k, int &pi, int &pk) {
+        int ai = 0, zi = coarse, ak = 0, zk = coarse;   // pre[a] <= i < pre[z]
+        while (zi - ai > 1 || zk - ak > 1) {
+            const int mi = (ai + zi) >> 1, mk = (ak + zk) >> 1;
+            const bool li = (int)pre[mi] <= i, lk = (int)pre[mk] <= k;
+            if (zi - ai > 1) (li ? ai : zi) = mi;
+            if (zk - ak > 1) (lk ? ak : zk) = mk;
         }
-        int left = i - (int)pre[a], wd = a * kCoarse;
-        for (;; ++wd) {
-            const int k = __popc(bits[wd]);
-            if (left < k) break;
-            left -= k;
-        }
-        return wd * 32 + nth_bit(bits[wd], left);
+        pi = pick(bits, ai, i - (int)pre[ai], words);
+        pk = pick(bits, ak, k - (int)pre[ak], words);
     };
 
-    // ---- moves, an equal share of the pairs for each block
+    // ---- moves, an equal share of the pairs for each block and, in runs of up
+    // to 32, for each warp: a lane locates one pair, then the warp copies them
+    // one row of K and one of V after the other, kBatch pieces a lane in flight
     const int m0 = (int)((long long)m * rank / CS), m1 = (int)((long long)m * (rank + 1) / CS);
-    const int vecs = p.D / 8;                           // 16-byte pieces of a row
+    const int lpp = p.D / 4;                            // lanes a pair: 16-byte pieces of a K and a V row
+    const int pp = 32 / lpp, sub = lane / lpp, piece = lane % lpp;
     const int slot_mask = (1 << p.page_shift) - 1;
-    for (int i0 = m0; i0 < m1; i0 += kPairs) {
-        const int np = min(kPairs, m1 - i0);
-        __syncthreads();
-        for (int i = tid; i < np; i += kThreads) {
-            const int to = locate(i0 + i), at = locate(m + i0 + i);
-            w_out[to] = w[at];
-            born_out[to] = born[at];
-            const int pt = page_of(p, b, to), pa = page_of(p, b, at);
-            const bool ok = pt < p.num_pages && pa < p.num_pages;
-            sh.pairs[0][i] = ok ? (pt << p.page_shift) | (to & slot_mask) : -1;
-            sh.pairs[1][i] = ok ? (pa << p.page_shift) | (at & slot_mask) : -1;
+    __nv_bfloat16 *cache = piece < lpp / 2 ? e.k_cache : e.v_cache;
+    cache += (long long)hk * p.D + (piece % (lpp / 2)) * 8;
+    const int run = min(32, (m1 - m0 + kWarps - 1) / kWarps);
+    for (int i0 = m0 + warp * run; i0 < m1; i0 += kWarps * run) {
+        const int np = min(run, m1 - i0);
+        long long to_at = -1, from_at = 0;              // elements from the cache's start
+        if (lane < np) {
+            int to, from;
+            locate(i0 + lane, m + i0 + lane, to, from);
+            const int et = page_entry(p, b, to), ef = page_entry(p, b, from);
+            const float x = __ldcg(w + from);
+            const int a = __ldcg(born + from);
+            w_out[to] = x;
+            born_out[to] = a;
+            const int pt = page_checked(p, et), pf = page_checked(p, ef);
+            if (pt < p.num_pages && pf < p.num_pages) {
+                to_at = pt * p.page_stride + (to & slot_mask) * p.k_stride;
+                from_at = pf * p.page_stride + (from & slot_mask) * p.k_stride;
+            }
         }
-        __syncthreads();
-        constexpr int kUnroll = 4;
-        const int items = np * 2 * vecs;
-        for (int x0 = tid; x0 < items; x0 += kUnroll * kThreads) {
-            uint4 val[kUnroll];
-            uint4 *dst[kUnroll];
+        for (int q = 0; q < np; q += kBatch * pp) {
+            uint4 val[kBatch];
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int x = x0 + u * kThreads;
-                dst[u] = nullptr;
-                if (x < items) {
-                    const int i = x / (2 * vecs), r = x % (2 * vecs);
-                    const int to = sh.pairs[0][i], at = sh.pairs[1][i];
-                    if (to >= 0) {
-                        __nv_bfloat16 *cache = r < vecs ? e.k_cache : e.v_cache;
-                        const long long in_row = (long long)hk * p.D + (r % vecs) * 8;
-                        dst[u] = reinterpret_cast<uint4 *>(cache + (long long)(to >> p.page_shift) * p.page_stride +
-                                                           (long long)(to & slot_mask) * p.k_stride + in_row);
-                        val[u] = *reinterpret_cast<const uint4 *>(
-                            cache + (long long)(at >> p.page_shift) * p.page_stride +
-                            (long long)(at & slot_mask) * p.k_stride + in_row);
-                    }
-                }
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = q + u * pp + sub;
+                const long long from = __shfl_sync(0xffffffffu, from_at, i & 31);
+                const long long to = __shfl_sync(0xffffffffu, to_at, i & 31);
+                if (i < np && to >= 0) val[u] = *reinterpret_cast<const uint4 *>(cache + from);
             }
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u)
-                if (dst[u]) *dst[u] = val[u];
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = q + u * pp + sub;
+                const long long to = __shfl_sync(0xffffffffu, to_at, i & 31);
+                if (i < np && to >= 0) *reinterpret_cast<uint4 *>(cache + to) = val[u];
+            }
         }
     }
 }
@@ -366,7 +429,11 @@ cudaError_t evict_prepare() {
 namespace {
 
 cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
-    const int cs = 1;
+    // A cluster per unit: as many blocks as fill the device, but no slice
+    // under 1024 keys
+    const long long units = (long long)p.B_max * p.Hkv;
+    int cs = 1;
+    while (cs < kMaxCluster && units * cs * 2 <= 148 * kBlocksPerSm && p.s_max >= 2048 * cs) cs *= 2;
     e.slice_words = slice_words(p.s_max, cs);
     const size_t fixed = sizeof(Head) + bits_bytes(p.s_max, cs), ranks = (size_t)e.slice_words * 32 * 4;
     e.cached = fixed + ranks <= (size_t)kMaxSmem ? e.slice_words * 32 : 0;
