@@ -188,10 +188,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
         return;
     }
     const int last = seen - e.recent;
-    auto read_rank = [&](int j) -> uint32_t {
-        const int a = __ldcg(born + j);
-        return order_of(__ldcg(w + j), a < e.sink || a >= last);
-    };
     const bool cached = e.cached >= per * 32;
     for (int i = tid; i < 256 * kCopies; i += kThreads) sh.hist[0][i] = 0;
     // one pass over the ledger: ranks into shared memory, entries below c to
@@ -216,7 +212,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
                 }
             }
         }
-    auto rank_of = [&](int j) -> uint32_t { return cached ? body[j - lo] : read_rank(j); };
+    // the ranks of kBatch keys of a thread, kThreads apart; past the slice's
+    // end `none`
+    auto read_ranks = [&](int j0, uint32_t none, uint32_t (&u)[kBatch]) {
+        if (cached) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) u[i] = j0 + i * kThreads < hi ? body[j0 + i * kThreads - lo] : none;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int j = j0 + i * kThreads;
+                const int a = j < hi ? __ldcg(born + j) : 0;
+                const float x = j < hi ? __ldcg(w + j) : 0.f;
+                u[i] = j < hi ? order_of(x, a < e.sink || a >= last) : none;
+            }
+        }
+    };
     __syncthreads();
 
     // ---- the c-th largest rank: after the passes, the ranks above it are those
@@ -226,10 +237,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     for (int pass = 0; pass < 4 && ties != need; ++pass) {
         shift -= 8;
         uint32_t *hist = sh.hist[pass & 1];
-        for (int j = lo + tid; j < hi; j += kThreads) {
-            const uint32_t u = rank_of(j);
-            if (pass == 0 || (u >> (shift + 8)) == prefix)
-                atomicAdd(&hist[((u >> shift) & 255u) * kCopies + (lane % kCopies)], 1u);
+        for (int j0 = lo + tid; j0 < hi; j0 += kBatch * kThreads) {
+            uint32_t u[kBatch];
+            read_ranks(j0, 0u, u);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (j0 + i * kThreads < hi && (pass == 0 || (u[i] >> (shift + 8)) == prefix))
+                    atomicAdd(&hist[((u[i] >> shift) & 255u) * kCopies + (lane % kCopies)], 1u);
         }
         __syncthreads();
         uint32_t mine = 0;
@@ -284,39 +298,56 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     }
 
     // ---- bits: kept if above the threshold, or one of its first `need` ties.
-    // Each warp takes a contiguous run of words; ties before it are counted
-    // first where not all of them stay.
-    const int wpw = (w1 - w0 + kWarps - 1) / kWarps;
-    const int ww0 = min(w1, w0 + warp * wpw), ww1 = min(w1, ww0 + wpw);
-    int tie_at = 0;
-    if (ties != need) {
-        int t = 0;
+    // A bit says evicted below c and kept from c on: the ones below c are the
+    // places to fill, the ones above the keys that fill them.  They go behind
+    // the ranks, which other warps still read.
+    uint32_t *bits = body + (cached ? e.cached : 0);
+    uint32_t *pre = bits + e.slice_words * CS;          // [slice_words CS / kCoarse + 2] prefix counts
+    const bool all_ties = ties == need;
+    for (int j0 = lo + tid; j0 - lane < hi; j0 += kBatch * kThreads) {
+        uint32_t u[kBatch];
+        read_ranks(j0, 0u, u);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int j = j0 + i * kThreads, first = j - lane;          // the word's first key
+            if (first < hi) {
+                const uint32_t r = shift < 32 ? u[i] >> shift : 0u;
+                const uint32_t kept = __ballot_sync(0xffffffffu, j < hi && (r > prefix || (all_ties && r == prefix)));
+                const uint32_t below = c - first >= 32 ? 0xffffffffu : c > first ? (1u << (c - first)) - 1u : 0u;
+                if (lane == 0) bits[first / 32] = kept ^ below;
+            }
+        }
+    }
+    if (!all_ties) {
+        // the first ties in order (shift is 0 here): each warp a run of words,
+        // after the ties of the runs and, from their last digit's counts, of
+        // the blocks before it
+        __syncthreads();
+        const int wpw = (w1 - w0 + kWarps - 1) / kWarps;
+        const int ww0 = min(w1, w0 + warp * wpw), ww1 = min(w1, ww0 + wpw);
+        auto rank_at = [&](int j) -> uint32_t {
+            if (cached) return body[j - lo];
+            const int a = __ldcg(born + j);
+            return order_of(__ldcg(w + j), a < e.sink || a >= last);
+        };
+        int before = 0;
         for (int wd = ww0; wd < ww1; ++wd) {
             const int j = wd * 32 + lane;
-            t += __popc(__ballot_sync(0xffffffffu, j < hi && rank_of(j) == prefix));   // shift is 0 here
+            before += __popc(__ballot_sync(0xffffffffu, j < hi && rank_at(j) == prefix));
         }
+        if (lane == 0) sh.scratch[warp] = before;
         __syncthreads();
-        if (lane == 0) sh.scratch[warp] = t;
-        __syncthreads();
-        for (int i = 0; i < warp; ++i) tie_at += sh.scratch[i];
-        // lower ranks' ties: their counts of the last digit
-        for (int r = 0; r < rank; ++r) tie_at += (int)cluster.map_shared_rank(&sh.count[3][prefix & 255u], r)[0];
-    }
-    // the unit's bits go behind the ranks (other blocks still need theirs)
-    uint32_t *bits = body + (cached ? e.cached : 0);
-    uint32_t *pre = bits + e.slice_words * CS;          // [slice_words CS / kCoarse + 1] evicted below c, kept above
-    for (int wd = ww0; wd < ww1; ++wd) {
-        const int j = wd * 32 + lane;
-        const uint32_t u = j < hi ? rank_of(j) >> shift : 0u;
-        const uint32_t above = __ballot_sync(0xffffffffu, j < hi && u > prefix);
-        const uint32_t tie = __ballot_sync(0xffffffffu, j < hi && u == prefix);
-        const bool in = (above >> lane & 1u) ||
-                        ((tie >> lane & 1u) && tie_at + __popc(tie & ((1u << lane) - 1u)) < need);
-        const uint32_t kept = __ballot_sync(0xffffffffu, in);
-        tie_at += __popc(tie);
-        // the bit of interest: evicted where j < c, kept where j >= c
-        const uint32_t below = c - wd * 32 >= 32 ? 0xffffffffu : c > wd * 32 ? (1u << (c - wd * 32)) - 1u : 0u;
-        if (lane == 0) bits[wd] = kept ^ below;
+        before = 0;
+        for (int i = 0; i < warp; ++i) before += sh.scratch[i];
+        for (int r = 0; r < rank; ++r) before += (int)*cluster.map_shared_rank(&sh.count[3][prefix & 255u], r);
+        for (int wd = ww0; wd < ww1; ++wd) {
+            const int j = wd * 32 + lane;
+            const uint32_t tie = __ballot_sync(0xffffffffu, j < hi && rank_at(j) == prefix);
+            const uint32_t kept = __ballot_sync(
+                0xffffffffu, (tie >> lane & 1u) && before + __popc(tie & ((1u << lane) - 1u)) < need);
+            before += __popc(tie);
+            if (lane == 0) bits[wd] ^= kept;
+        }
     }
     // ---- every block gets the whole unit's bits
     if (CS > 1) {
