@@ -61,6 +61,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libvgqa.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -151,23 +153,32 @@ def _check(code: int, where: str):
         raise AttnError(code, where)
 
 
-def _stream_ptr(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+# the current stream's handle without building a Stream object (3 us a call),
+# where this torch has the shortcut
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_ptr(stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(_raw_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 _ROPE_DTYPES = {torch.bfloat16: ATTN_DTYPE_BF16, torch.float16: ATTN_DTYPE_F16, torch.float32: ATTN_DTYPE_F32}
 
 
-def _heads_strided(name, t, H, D, dev):
-    """Token stride of t [T, H, D] whose heads are contiguous within a token."""
+def _heads_strided(name, t, T, H, D, dev):
+    """Address and token stride of t [T, H, D] on device `dev` whose heads are
+    contiguous within a token."""
+    if t.get_device() != dev or t.shape != (T, H, D):
+        raise ValueError(f"{name} must be a tensor [{T}, {H}, {D}] of CUDA device {dev}")
     s = t.stride()
-    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D or t.get_device() != dev:
-        raise ValueError(f"{name} must be a tensor [T, {H}, {D}] of CUDA device {dev}")
     if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
         raise ValueError(f"{name} must keep each token's heads contiguous (strides (s, D, 1), s >= H*D)")
-    return s[0] if t.shape[0] > 1 else max(s[0], H * D)
+    return t.data_ptr(), s[0] if T > 1 else max(s[0], H * D)
 
 
 def rope_table(n_pairs, sections=None, *, base=10000.0, restart=False):
@@ -219,12 +230,14 @@ class Rope:
 
     def _pos(self, pos, T, dev):
         """Address and axis stride of pos [n_axes, T] (or [T] for one axis)."""
-        if pos.dim() == 1 and self.n_axes == 1:
+        n = self.n_axes
+        if n == 1 and pos.dim() == 1:
             pos = pos[None]
-        if pos.dtype != torch.int32 or pos.get_device() != dev or pos.dim() != 2 or pos.shape[0] != self.n_axes or \
-                pos.shape[1] != T or (T > 1 and pos.stride(1) != 1):
-            raise ValueError(f"pos must be int32 [{self.n_axes}, {T}] on CUDA device {dev}, unit stride over tokens")
-        return pos.data_ptr(), max(pos.stride(0), T) if self.n_axes == 1 else pos.stride(0)
+        if pos.dtype is torch.int32 and pos.get_device() == dev and pos.shape == (n, T):
+            s = pos.stride()
+            if T <= 1 or s[1] == 1:
+                return pos.data_ptr(), s[0] if n > 1 else max(s[0], T)
+        raise ValueError(f"pos must be int32 [{n}, {T}] on CUDA device {dev}, unit stride over tokens")
 
     def apply(self, x, pos, out=None, *, grad=False, stream=None):
         """out = rope.apply(x, pos[, out, grad, stream]): rotate x [T, H, D]
@@ -237,22 +250,23 @@ class Rope:
         dtype = _ROPE_DTYPES.get(x.dtype)
         if dtype is None:
             raise TypeError("x must be bf16, fp16 or fp32")
-        dev = torch.cuda.current_device()
+        dev = _raw_device()
         if x.dim() != 3:
             raise ValueError("x must be [T, H, D]")
-        T, H, _ = x.shape
-        xs = _heads_strided("x", x, H, self.D, dev)
+        T, H, D = x.shape[0], x.shape[1], self.D
+        xp, xs = _heads_strided("x", x, T, H, D, dev)
         if out is None:
-            out = torch.empty(T, H, self.D, dtype=x.dtype, device=x.device)
-        if out.dtype != x.dtype or out.shape != x.shape:
+            out = torch.empty(T, H, D, dtype=x.dtype, device=x.device)
+        if out.dtype is not x.dtype:
             raise ValueError("out must have x's type and shape")
-        os_ = _heads_strided("out", out, H, self.D, dev)
+        op, os_ = _heads_strided("out", out, T, H, D, dev)
         pp, ps = self._pos(pos, T, dev)
         if T == 0 or H == 0:
             return out
-        rc = lib().attn_rope_apply(self._h, dtype, x.data_ptr(), xs, T, H, pp, ps, 1 if grad else 0, out.data_ptr(),
-                                   os_, _stream_ptr(stream))
-        _check(rc, "attn_rope_apply")
+        rc = lib().attn_rope_apply(self._h, dtype, xp, xs, T, H, pp, ps, 1 if grad else 0, op, os_,
+                                   _stream_ptr(stream))
+        if rc:
+            _check(rc, "attn_rope_apply")
         return out
 
     def close(self):
@@ -293,6 +307,7 @@ class Plan:
         self._h = h
         self.device = torch.cuda.current_device()
         self.info = self._info()
+        self._sizes = (*(self.info[n] for n in ("B_max", "Hq", "Hkv", "D")), self.device, self.info["s_max"])
 
     def _info(self) -> dict:
         d = PlanDesc()
@@ -374,45 +389,51 @@ class Plan:
         return out, lse
 
     def _paging(self, k_cache, v_cache, block_table):
-        """The cache arguments of the paged entry points, in the C ABI's order
-        (v_cache None: keys only)."""
-        i = self.info
+        """Addresses of the caches (v_cache None: keys only) and the cache
+        arguments of the paged entry points, in the C ABI's order."""
+        B, _, Hkv, D, dev, s_max = self._sizes
         shape, s = k_cache.shape, k_cache.stride()
-        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-            if t is None:
-                continue
-            if t.dtype != torch.bfloat16 or t.get_device() != self.device:
-                raise TypeError(f"{name} must be a bf16 tensor of the plan's device")
-            if t.dim() != 4 or t.shape[2] != i["Hkv"] or t.shape[3] != i["D"]:
-                raise ValueError(f"{name} must be [num_pages, page_size, {i['Hkv']}, {i['D']}]")
-            if t.stride(3) != 1 or (i["Hkv"] > 1 and t.stride(2) != i["D"]):
-                raise ValueError(f"{name} must keep each token's heads contiguous")
-            if t.shape != shape or t.stride() != s:
+        if k_cache.dtype is not torch.bfloat16 or k_cache.get_device() != dev:
+            raise TypeError("k_cache must be a bf16 tensor of the plan's device")
+        if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
+            raise ValueError(f"k_cache must be [num_pages, page_size, {Hkv}, {D}]")
+        if s[3] != 1 or (Hkv > 1 and s[2] != D):
+            raise ValueError("k_cache must keep each token's heads contiguous")
+        vp = None
+        if v_cache is not None:
+            if v_cache.dtype is not torch.bfloat16 or v_cache.get_device() != dev:
+                raise TypeError("v_cache must be a bf16 tensor of the plan's device")
+            if v_cache.shape != shape or v_cache.stride() != s:
                 raise ValueError("k_cache and v_cache must have the same shape and strides")
+            vp = v_cache.data_ptr()
         n_pages, page_size = shape[0], shape[1]
-        tok = s[1] if page_size > 1 else i["Hkv"] * i["D"]
-        bt = block_table
-        if bt.dtype != torch.int32 or bt.get_device() != self.device or bt.dim() != 2 or bt.shape[0] != i["B_max"] or \
-                (bt.shape[1] > 1 and bt.stride(1) != 1):
+        tok = s[1] if page_size > 1 else Hkv * D
+        bt, bs = block_table.shape, block_table.stride()
+        if block_table.dtype is not torch.int32 or block_table.get_device() != dev or len(bt) != 2 or bt[0] != B or \
+                (bt[1] > 1 and bs[1] != 1):
             raise ValueError("block_table must be an int32 tensor [B_max, n] of the plan's device, unit column stride")
-        if bt.shape[1] * page_size < i["s_max"]:
+        if bt[1] * page_size < s_max:
             raise ValueError("block_table rows must cover s_max keys")
-        return (s[0] if n_pages > 1 else page_size * tok, tok, page_size, n_pages, bt.data_ptr(),
-                bt.stride(0) if bt.shape[0] > 1 else max(bt.stride(0), bt.shape[1]))
+        return k_cache.data_ptr(), vp, (s[0] if n_pages > 1 else page_size * tok, tok, page_size, n_pages,
+                                        block_table.data_ptr(), bs[0] if B > 1 else max(bs[0], bt[1]))
 
     def _per_sequence(self, name, t, n):
-        if t.dtype != torch.int32 or t.get_device() != self.device or t.numel() != n or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on the plan's device")
-        return t.data_ptr()
+        if t.dtype is torch.int32 and t.get_device() == self.device and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on the plan's device")
 
-    def _ledger(self, name, t, dtype, ld):
-        """Address of a ledger array [B_max, Hkv, ld]."""
-        i = self.info
-        if t.dtype != dtype or t.get_device() != self.device or not t.is_contiguous() or t.dim() != 3 or \
-                t.shape[0] != i["B_max"] or t.shape[1] != i["Hkv"] or t.shape[2] != ld or ld < i["s_max"]:
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor [{i['B_max']}, {i['Hkv']}, >= {i['s_max']}] "
-                             "of the plan's device (one length for the whole ledger)")
-        return t.data_ptr()
+    def _ledger(self, name, t, dtype, shape):
+        """Address of a ledger array of `shape` [B_max, Hkv, ld >= s_max]."""
+        if t.dtype is dtype and t.get_device() == self.device and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} of the plan's device")
+
+    def _ledger_shape(self, name, t):
+        shape = t.shape
+        B, _, Hkv, _, _, s_max = self._sizes
+        if len(shape) != 3 or shape[0] != B or shape[1] != Hkv or shape[2] < s_max:
+            raise ValueError(f"{name} must be [{B}, {Hkv}, >= {s_max}]")
+        return shape
 
     def append_paged(self, k, v, k_cache, v_cache, block_table, cu_q, cu_k, *, q=None, pos=None, rope=None,
                      q_out=None, stream=None):
@@ -426,65 +447,64 @@ class Plan:
         through attn_append_paged."""
         if self._h is None:
             raise AttnError(-5, "attn_append_paged")
-        i, dev = self.info, self.device
+        B, Hq, Hkv, D, dev, _ = self._sizes
         T = k.shape[0]
-        if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or v.shape[0] != T:
-            raise TypeError("k and v must be bf16 tensors of the same tokens")
-        ks, vs = _heads_strided("k", k, i["Hkv"], i["D"], dev), _heads_strided("v", v, i["Hkv"], i["D"], dev)
-        qp = op = None
-        qs = 0
+        if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
+            raise TypeError("k and v must be bf16 tensors")
+        kp, ks = _heads_strided("k", k, T, Hkv, D, dev)
+        vp, vs = _heads_strided("v", v, T, Hkv, D, dev)
+        qp = op = rp = pp = None
+        qs = ps = 0
         if q is not None:
-            if q.dtype != torch.bfloat16 or q.shape[0] != T:
-                raise TypeError("q must be a bf16 tensor of the same tokens as k")
-            qs = _heads_strided("q", q, i["Hq"], i["D"], dev)
+            if q.dtype is not torch.bfloat16:
+                raise TypeError("q must be a bf16 tensor")
+            qp, qs = _heads_strided("q", q, T, Hq, D, dev)
             if q_out is None:
-                q_out = torch.empty(T, i["Hq"], i["D"], dtype=torch.bfloat16, device=q.device)
-            if q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or not q_out.is_contiguous() or \
+                q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+            if q_out.dtype is not torch.bfloat16 or q_out.shape != (T, Hq, D) or not q_out.is_contiguous() or \
                     q_out.get_device() != dev:
                 raise ValueError("q_out must be a contiguous bf16 tensor shaped like q, on its device")
-            qp, op = q.data_ptr(), q_out.data_ptr()
+            op = q_out.data_ptr()
         elif q_out is not None:
             raise ValueError("q_out without q")
-        rp = pp = None
-        ps = 0
         if rope is not None:
-            if rope.handle is None:
+            rp = rope._h
+            if rp is None:
                 raise AttnError(-3, "attn_append_paged")
             if pos is None:
                 raise ValueError("rope needs pos")
-            rp = rope.handle
             pp, ps = rope._pos(pos, T, dev)
         elif pos is not None:
             raise ValueError("pos without rope")
-        cq, ck = self._per_sequence("cu_q", cu_q, i["B_max"] + 1), self._per_sequence("cu_k", cu_k, i["B_max"] + 1)
-        cache = self._paging(k_cache, v_cache, block_table)
+        cq, ck = self._per_sequence("cu_q", cu_q, B + 1), self._per_sequence("cu_k", cu_k, B + 1)
+        kc, vc, cache = self._paging(k_cache, v_cache, block_table)
         if T:
-            rc = lib().attn_append_paged(self._h, rp, qp, qs, k.data_ptr(), ks, v.data_ptr(), vs, T, pp, ps, op,
-                                         k_cache.data_ptr(), v_cache.data_ptr(), *cache, cq, ck, _stream_ptr(stream))
-            _check(rc, "attn_append_paged")
+            rc = lib().attn_append_paged(self._h, rp, qp, qs, kp, ks, vp, vs, T, pp, ps, op, kc, vc, *cache, cq, ck,
+                                         _stream_ptr(stream))
+            if rc:
+                _check(rc, "attn_append_paged")
         return q_out
 
     def _weights_args(self, q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream):
-        i, dev = self.info, self.device
-        if q.dtype != torch.bfloat16 or q.get_device() != dev or not q.is_contiguous():
-            raise TypeError("q must be a contiguous bf16 tensor of the plan's device")
-        if q.dim() != 3 or q.shape[1] != i["Hq"] or q.shape[2] != i["D"]:
-            raise ValueError(f"q must be [T_q, {i['Hq']}, {i['D']}]")
-        if lse.dtype != torch.float32 or lse.get_device() != dev or not lse.is_contiguous() or \
-                lse.dim() != 2 or lse.shape[0] != q.shape[0] or lse.shape[1] != i["Hq"]:
+        B, Hq, Hkv, D, dev, s_max = self._sizes
+        T = q.shape[0]
+        if q.dtype is not torch.bfloat16 or q.get_device() != dev or q.shape != (T, Hq, D) or not q.is_contiguous():
+            raise ValueError(f"q must be a contiguous bf16 tensor [T_q, {Hq}, {D}] of the plan's device")
+        if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or \
+                not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 tensor [T_q, Hq] of the plan's device")
         if (seen is None) != (born is None):
             raise ValueError("seen and born go together")
         first = out if out is not None else weight_in if weight_in is not None else born
-        ld = first.shape[-1] if first is not None else i["s_max"]
+        shape = (B, Hkv, s_max) if first is None else self._ledger_shape("the ledger", first)
         if out is None:
-            out = torch.zeros(i["B_max"], i["Hkv"], ld, dtype=torch.float32, device=q.device)
-        ledger = (self._per_sequence("cu_q", cu_q, i["B_max"] + 1), self._per_sequence("cu_k", cu_k, i["B_max"] + 1),
+            out = torch.zeros(shape, dtype=torch.float32, device=q.device)
+        ledger = (self._per_sequence("cu_q", cu_q, B + 1), self._per_sequence("cu_k", cu_k, B + 1),
                   lse.data_ptr(), decay,
-                  None if weight_in is None else self._ledger("weight_in", weight_in, torch.float32, ld),
-                  self._ledger("out", out, torch.float32, ld), ld,
-                  None if seen is None else self._per_sequence("seen", seen, i["B_max"]),
-                  None if born is None else self._ledger("born", born, torch.int32, ld), _stream_ptr(stream))
+                  None if weight_in is None else self._ledger("weight_in", weight_in, torch.float32, shape),
+                  self._ledger("out", out, torch.float32, shape), shape[2],
+                  None if seen is None else self._per_sequence("seen", seen, B),
+                  None if born is None else self._ledger("born", born, torch.int32, shape), _stream_ptr(stream))
         return out, ledger
 
     def key_weights(self, q, k, cu_q, cu_k, lse, weight_in=None, *, decay=1.0, out=None, seen=None, born=None,
@@ -499,12 +519,14 @@ class Plan:
         attn_key_weights."""
         if self._h is None:
             raise AttnError(-5, "attn_key_weights")
-        i = self.info
-        if k.dtype != torch.bfloat16:
-            raise TypeError("k must be a bf16 CUDA tensor")
-        ks = _heads_strided("k", k, i["Hkv"], i["D"], self.device)
+        _, _, Hkv, D, dev, _ = self._sizes
+        if k.dtype is not torch.bfloat16:
+            raise TypeError("k must be a bf16 tensor")
+        kp, ks = _heads_strided("k", k, k.shape[0], Hkv, D, dev)
         out, ledger = self._weights_args(q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream)
-        _check(lib().attn_key_weights(self._h, q.data_ptr(), k.data_ptr(), ks, *ledger), "attn_key_weights")
+        rc = lib().attn_key_weights(self._h, q.data_ptr(), kp, ks, *ledger)
+        if rc:
+            _check(rc, "attn_key_weights")
         return out
 
     def key_weights_paged(self, q, k_cache, block_table, cu_q, cu_k, lse, weight_in=None, *, decay=1.0, out=None,
@@ -513,10 +535,11 @@ class Plan:
         run_paged).  Goes through attn_key_weights_paged."""
         if self._h is None:
             raise AttnError(-5, "attn_key_weights_paged")
-        cache = self._paging(k_cache, None, block_table)
+        kc, _, cache = self._paging(k_cache, None, block_table)
         out, ledger = self._weights_args(q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream)
-        _check(lib().attn_key_weights_paged(self._h, q.data_ptr(), k_cache.data_ptr(), *cache, *ledger),
-               "attn_key_weights_paged")
+        rc = lib().attn_key_weights_paged(self._h, q.data_ptr(), kc, *cache, *ledger)
+        if rc:
+            _check(rc, "attn_key_weights_paged")
         return out
 
     def evict_paged(self, weight, born, seen, keep, k_cache, v_cache, block_table, cu_k, *, sink=0, recent=0,
@@ -533,21 +556,27 @@ class Plan:
         attn_evict_paged."""
         if self._h is None:
             raise AttnError(-5, "attn_evict_paged")
-        i = self.info
-        ld = weight.shape[-1]
-        weight_out = weight if weight_out is None else weight_out
-        born_out = born if born_out is None else born_out
+        B = self._sizes[0]
+        shape = self._ledger_shape("weight", weight)
+        wp, bp = self._ledger("weight", weight, torch.float32, shape), self._ledger("born", born, torch.int32, shape)
+        wo, bo = wp, bp
+        if weight_out is None:
+            weight_out = weight
+        else:
+            wo = self._ledger("weight_out", weight_out, torch.float32, shape)
+        if born_out is None:
+            born_out = born
+        else:
+            bo = self._ledger("born_out", born_out, torch.int32, shape)
         if cu_k_out is None:
             cu_k_out = torch.empty_like(cu_k)
-        cache = self._paging(k_cache, v_cache, block_table)
-        rc = lib().attn_evict_paged(
-            self._h, self._ledger("weight", weight, torch.float32, ld), self._ledger("born", born, torch.int32, ld),
-            self._per_sequence("seen", seen, i["B_max"]), self._per_sequence("keep", keep, i["B_max"]), int(sink),
-            int(recent), self._ledger("weight_out", weight_out, torch.float32, ld),
-            self._ledger("born_out", born_out, torch.int32, ld), ld, k_cache.data_ptr(), v_cache.data_ptr(), *cache,
-            self._per_sequence("cu_k", cu_k, i["B_max"] + 1), self._per_sequence("cu_k_out", cu_k_out, i["B_max"] + 1),
-            _stream_ptr(stream))
-        _check(rc, "attn_evict_paged")
+        kc, vc, cache = self._paging(k_cache, v_cache, block_table)
+        rc = lib().attn_evict_paged(self._h, wp, bp, self._per_sequence("seen", seen, B),
+                                    self._per_sequence("keep", keep, B), sink, recent, wo, bo, shape[2], kc, vc, *cache,
+                                    self._per_sequence("cu_k", cu_k, B + 1),
+                                    self._per_sequence("cu_k_out", cu_k_out, B + 1), _stream_ptr(stream))
+        if rc:
+            _check(rc, "attn_evict_paged")
         return weight_out, born_out, cu_k_out
 
     def _check_common(self, q, cu_q, cu_k, out, lse, where):
