@@ -4,11 +4,11 @@
 // (attn_append_paged).  The mathematics is in rope.cuh.
 //
 // Both are bound by memory: each element is read once and written once.  A
-// block takes a few whole tokens; it computes the cosines and sines of their
-// pairs once into shared memory (64-bit integer angle and sincospif, about 40
-// instructions a pair) and every head of those tokens reuses them.  A thread
-// then moves V pairs at a time, two 16-byte loads and two 16-byte stores,
-// several heads in flight at once.
+// block takes a few tokens at a time; it computes the cosines and sines of
+// their pairs once into shared memory (64-bit integer angle and sincospif,
+// about 40 instructions a pair), and a thread keeps those of its token and its
+// V pairs in registers while it goes through some of the token's heads: two
+// 16-byte loads and two 16-byte stores a head, several heads in flight.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -27,56 +27,88 @@ namespace vgqa {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 4;                // rows (token, head) of a thread in flight
+constexpr int kThreads = 256;             // at most; a block has what its tokens need
+constexpr int kBlocksPerSm = 4;
+constexpr int kUnroll = 3;                // heads of a thread in flight at once
+constexpr int kMaxHeads = 3;              // heads a thread goes through, unless there are too many
+constexpr int kAppendUnroll = 2;          // and in an append, whose registers also hold addresses
+constexpr int kAppendHeads = 5;
 constexpr int kMaxFactors = 2048;         // (cos, sin) pairs of a block's tokens: 16 KB
 
-template <typename T, int V, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeTable tab, const T *x,
-                                                        long long xs, long long n_tok, int H, int D,
-                                                        const int32_t *__restrict__ pos, long long ps, float sign,
-                                                        T *out, long long os, int tpb, int groups) {
-    extern __shared__ float2 cs[];            // [tpb][n]
-    const int n = tab.n;
-    const long long t0 = (long long)blockIdx.x * tpb;
-    const int nt = (int)min((long long)tpb, n_tok - t0);
-    for (int i = threadIdx.x; i < nt * n; i += kThreads) {
-        const int t = i / n, pr = i % n;
+// How threads are laid out: `groups` neighbours share a head, `lanes` heads
+// are worked on side by side, `tokens` tokens in a block.
+struct Shape {
+    int groups, lanes, tokens, threads;
+    long long blocks;
+};
+
+// Heads per thread: enough work to keep the factors' cost small, but a thread
+// per head while the whole call would not fill the device twice over.
+Shape shape_of(long long n_tok, int heads, int groups, int n, int most) {
+    Shape s;
+    s.groups = groups;
+    const long long fill = 2ll * 148 * kThreads * kBlocksPerSm;
+    const int each = (int)std::max(1ll, std::min<long long>(most, n_tok * heads * groups / fill));
+    s.lanes = std::min((heads + each - 1) / each, kThreads / groups);
+    s.tokens = std::max(1, std::min(kThreads / (groups * s.lanes), kMaxFactors / std::max(n, 1)));
+    s.tokens = (int)std::min<long long>(s.tokens, n_tok);
+    s.threads = (s.tokens * groups * s.lanes + 31) / 32 * 32;
+    s.blocks = (n_tok + s.tokens - 1) / s.tokens;
+    return s;
+}
+
+// the cosines and sines of tokens [t0, t0 + nt): cs[token][pair]
+__device__ __forceinline__ void fill_factors(const RopeTable &tab, float2 *cs, const int32_t *__restrict__ pos,
+                                             long long ps, long long t0, int nt, float sign) {
+    for (int i = threadIdx.x; i < nt * tab.n; i += blockDim.x) {
+        const int t = i / tab.n, pr = i - t * tab.n;
         cs[i] = rope_cos_sin(tab, pr, __ldg(pos + tab.axis[pr] * ps + t0 + t), sign);
     }
-    __syncthreads();
-    // thread = (group, row lane); rows = the tokens' heads
-    const int lanes = kThreads / groups;
-    const int g = threadIdx.x % groups, r0 = threadIdx.x / groups;
-    if (r0 >= lanes) return;
+}
+
+template <typename T, int V, bool HALF>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    rope_kernel(const __grid_constant__ RopeTable tab, const T *x, long long xs, long long n_tok, int H, int D,
+                const int32_t *__restrict__ pos, long long ps, float sign, T *out, long long os, int groups, int lanes,
+                int tokens) {
+    extern __shared__ float2 cs[];
+    const int n = tab.n;
+    const long long t0 = (long long)blockIdx.x * tokens;
+    const int nt = (int)min((long long)tokens, n_tok - t0);
+    const int g = threadIdx.x % groups, y = threadIdx.x / groups, lane = y % lanes, tok = y / lanes;
     int a, b;
     rope_offsets<V, HALF>(g, n, D, a, b);
-    const bool turn = g * V < n;
-    const int rows = nt * H;
+    const bool turn = g * V < n, live = tok < nt;
     using W = Vec<T, V>;
-    for (int r = r0; r < rows; r += kUnroll * lanes) {
-        W u[kUnroll], w[kUnroll];
-        int tok[kUnroll];
+    const T *src = x + (t0 + tok) * xs + a;
+    T *dst = out + (t0 + tok) * os + a;
+    const int d = b - a;                      // from the first access to the second
+    W u[kUnroll], w[kUnroll];
+    auto load = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int ri = r + i * lanes;
-            if (ri < rows) {
-                tok[i] = ri / H;
-                const T *src = x + (t0 + tok[i]) * xs + (long long)(ri - tok[i] * H) * D;
-                u[i] = *reinterpret_cast<const W *>(src + a);
-                if (b >= 0) w[i] = *reinterpret_cast<const W *>(src + b);
+        for (int i = 0; i < kUnroll; ++i)
+            if (live && h + i * lanes < H) {
+                u[i] = *reinterpret_cast<const W *>(src + (h + i * lanes) * D);
+                if (b >= 0) w[i] = *reinterpret_cast<const W *>(src + (h + i * lanes) * D + d);
             }
-        }
+    };
+    load(lane);                               // on its way while the factors are computed
+    fill_factors(tab, cs, pos, ps, t0, nt, sign);
+    __syncthreads();
+    if (!live) return;
+    float2 f[V];
+    if (turn)
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int ri = r + i * lanes;
-            if (ri < rows) {
-                if (turn) rope_rotate<T, V, HALF>(u[i], w[i], cs + tok[i] * n + g * V);
-                T *dst = out + (t0 + tok[i]) * os + (long long)(ri - tok[i] * H) * D;
-                *reinterpret_cast<W *>(dst + a) = u[i];
-                if (b >= 0) *reinterpret_cast<W *>(dst + b) = w[i];
+        for (int i = 0; i < V; ++i) f[i] = cs[tok * n + g * V + i];
+    for (int h = lane; h < H; h += kUnroll * lanes) {
+        if (h != lane) load(h);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            if (h + i * lanes < H) {
+                if (turn) rope_rotate<T, V, HALF>(u[i], w[i], f);
+                *reinterpret_cast<W *>(dst + (h + i * lanes) * D) = u[i];
+                if (b >= 0) *reinterpret_cast<W *>(dst + (h + i * lanes) * D + d) = w[i];
             }
-        }
     }
 }
 
@@ -88,113 +120,102 @@ struct Append {
     const int32_t *pos;
     long long pos_stride, qs, ks, vs;         // axis stride; token strides of q, k, v
     long long n_tok;
-    int tpb, groups;
+    int groups, lanes, tokens;
 };
 
 template <int V, bool HALF>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ RopeTable tab, const Params p,
-                                                          const Append ap) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    append_kernel(const __grid_constant__ RopeTable tab, const Params p, const Append ap) {
     using T = __nv_bfloat16;
     using W = Vec<T, V>;
-    extern __shared__ float2 cs[];            // [tpb][n], then [tpb] cache offsets, [tpb] sequences
-    const int n = tab.n, tpb = ap.tpb, tid = threadIdx.x;
-    long long *slot = reinterpret_cast<long long *>(cs + tpb * n);
-    int *seq = reinterpret_cast<int *>(slot + tpb);
-    const long long t0 = (long long)blockIdx.x * tpb;
-    const int nt = (int)min((long long)tpb, ap.n_tok - t0);
-
-    // the sequence of each token: the one whose range covers it
-    for (int i = tid; i < tpb; i += kThreads) seq[i] = -1;
-    __syncthreads();
-    for (int b = tid; b < p.B_max; b += kThreads) {
-        const long long lo = max((long long)__ldg(p.cu_q + b), t0), hi = min((long long)__ldg(p.cu_q + b + 1), t0 + nt);
-        for (long long t = lo; t < hi; ++t) seq[t - t0] = b;
-    }
-    for (int i = tid; i < nt * n; i += kThreads) {
-        const int t = i / n, pr = i % n;
-        cs[i] = rope_cos_sin(tab, pr, __ldg(ap.pos + tab.axis[pr] * ap.pos_stride + t0 + t), 1.f);
-    }
-    __syncthreads();
-    // where its key goes: -1 not at all (no sequence, or a rejected one), -2
-    // rotated but not stored (a bad table entry, or more queries than keys)
-    for (int i = tid; i < nt; i += kThreads) {
-        long long at = -1;
-        int q0, Lq, k0, Lk;
-        if (seq[i] >= 0 && load_lengths(p, seq[i], true, q0, Lq, k0, Lk)) {
-            const int j = Lk - Lq + (int)(t0 + i - q0);
-            at = -2;
-            if (j >= 0) {
-                const int page = page_of(p, seq[i], j);
-                if (page < p.num_pages)
-                    at = page * p.page_stride + (long long)(j & ((1 << p.page_shift) - 1)) * p.k_stride;
-            }
-        }
-        slot[i] = at;
-    }
-    // a sequence that has to be reported but owns no token of any block
-    if (blockIdx.x == 0)
-        for (int b = tid; b < p.B_max; b += kThreads) {
-            int q0, Lq, k0, Lk;
-            load_lengths(p, b, true, q0, Lq, k0, Lk);
-        }
-    __syncthreads();
-
-    const int lanes = kThreads / ap.groups;
-    const int g = tid % ap.groups, r0 = tid / ap.groups;
-    if (r0 >= lanes) return;
+    extern __shared__ float2 cs[];            // [tokens][n], then [tokens] cache offsets, [tokens] (sequence, key)
+    const int n = tab.n, tokens = ap.tokens, tid = threadIdx.x, D = p.D;
+    long long *slot = reinterpret_cast<long long *>(cs + tokens * n);
+    int2 *owner = reinterpret_cast<int2 *>(slot + tokens);
+    const long long t0 = (long long)blockIdx.x * tokens;
+    const int nt = (int)min((long long)tokens, ap.n_tok - t0);
+    const int lanes = ap.lanes;
+    const int g = tid % ap.groups, y = tid / ap.groups, lane = y % lanes, tok = y / lanes;
     int a, b;
-    rope_offsets<V, HALF>(g, n, p.D, a, b);
-    const bool turn = g * V < n;
-    const int nq = ap.q_out ? p.Hq : 0, heads = nq + 2 * p.Hkv, rows = nt * heads;
-    for (int r = r0; r < rows; r += kUnroll * lanes) {
-        W u[kUnroll], w[kUnroll];
-        T *dst[kUnroll];
-        int tok[kUnroll];
-        bool rot[kUnroll];
+    rope_offsets<V, HALF>(g, n, D, a, b);
+    const bool turn = g * V < n, live = tok < nt;
+    const int nq = ap.q_out ? p.Hq : 0, nkv = 2 * p.Hkv, d = b - a;
+    const long long t = t0 + tok;
+    W u[kAppendUnroll], w[kAppendUnroll];
+    // heads h0, h0 + lanes, ... below `heads` from `from(h)`
+    auto load = [&](int h0, int heads, auto from) {
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int ri = r + i * lanes;
-            dst[i] = nullptr;
-            if (ri < rows) {
-                tok[i] = ri / heads;
-                const int h = ri - tok[i] * heads, hk = h - nq;
-                const long long t = t0 + tok[i], at = slot[tok[i]];
-                const T *src;
-                rot[i] = turn && hk < p.Hkv;
-                if (hk < 0) {
-                    src = p.q + t * ap.qs + h * p.D;
-                    if (at != -1) dst[i] = ap.q_out + (t * p.Hq + h) * p.D;
-                } else if (hk < p.Hkv) {
-                    src = p.k + t * ap.ks + hk * p.D;
-                    if (at >= 0) dst[i] = ap.k_cache + at + hk * p.D;
-                } else {
-                    src = p.v + t * ap.vs + (hk - p.Hkv) * p.D;
-                    if (at >= 0) dst[i] = ap.v_cache + at + (hk - p.Hkv) * p.D;
-                }
-                if (dst[i]) {
-                    u[i] = *reinterpret_cast<const W *>(src + a);
-                    if (b >= 0) w[i] = *reinterpret_cast<const W *>(src + b);
-                }
+        for (int i = 0; i < kAppendUnroll; ++i)
+            if (h0 + i * lanes < heads) {
+                const T *src = from(h0 + i * lanes) + a;
+                u[i] = *reinterpret_cast<const W *>(src);
+                if (b >= 0) w[i] = *reinterpret_cast<const W *>(src + d);
             }
-        }
+    };
+    auto q_at = [&](int h) { return p.q + t * ap.qs + h * D; };
+    auto kv_at = [&](int h) { return h < p.Hkv ? p.k + t * ap.ks + h * D : p.v + t * ap.vs + (h - p.Hkv) * D; };
+    if (live) load(lane, nq, q_at);           // on its way while the places are looked up
+
+    // the sequence of each token, the one whose range covers it, and its key
+    for (int i = tid; i < tokens; i += blockDim.x) owner[i] = make_int2(-1, 0);
+    __syncthreads();
+    for (int s = tid; s < p.B_max; s += blockDim.x) {
+        int q0, Lq, k0, Lk;
+        if (!load_lengths(p, s, blockIdx.x == 0, q0, Lq, k0, Lk)) continue;
+        const int lo = (int)max(0ll, q0 - t0), hi = (int)min((long long)nt, q0 + Lq - t0);
+        for (int i = lo; i < hi; ++i) owner[i] = make_int2(s, (int)(Lk - Lq + (t0 + i - q0)));
+    }
+    fill_factors(tab, cs, ap.pos, ap.pos_stride, t0, nt, 1.f);
+    __syncthreads();
+    // each token's page is looked up while the queries go through
+    int entry = 0;
+    const int2 mine = tid < nt ? owner[tid] : make_int2(-1, 0);
+    if (mine.x >= 0 && mine.y >= 0) entry = page_entry(p, mine.x, mine.y);
+    float2 f[V];
+    if (live && turn)
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            if (dst[i]) {
-                if (rot[i]) rope_rotate<T, V, HALF>(u[i], w[i], cs + tok[i] * n + g * V);
-                *reinterpret_cast<W *>(dst[i] + a) = u[i];
-                if (b >= 0) *reinterpret_cast<W *>(dst[i] + b) = w[i];
+        for (int i = 0; i < V; ++i) f[i] = cs[tok * n + g * V + i];
+    const bool owned = live && owner[tok].x >= 0;
+    for (int h0 = lane; owned && h0 < nq; h0 += kAppendUnroll * lanes) {
+        if (h0 != lane) load(h0, nq, q_at);
+#pragma unroll
+        for (int i = 0; i < kAppendUnroll; ++i)
+            if (h0 + i * lanes < nq) {
+                T *dst = ap.q_out + (t * p.Hq + h0 + i * lanes) * D + a;
+                if (turn) rope_rotate<T, V, HALF>(u[i], w[i], f);
+                *reinterpret_cast<W *>(dst) = u[i];
+                if (b >= 0) *reinterpret_cast<W *>(dst + d) = w[i];
+            }
+    }
+    if (owned) load(lane, nkv, kv_at);
+    // where the key goes, or -1: no sequence, a bad table entry, or a query
+    // before the first key
+    if (tid < nt) {
+        long long at = -1;
+        if (mine.x >= 0 && mine.y >= 0) {
+            const int page = page_checked(p, entry);
+            if (page < p.num_pages)
+                at = page * p.page_stride + (long long)(mine.y & ((1 << p.page_shift) - 1)) * p.k_stride;
+        }
+        slot[tid] = at;
+    }
+    __syncthreads();
+    if (!owned) return;
+    const long long at = slot[tok];
+    if (at < 0) return;
+    for (int h0 = lane; h0 < nkv; h0 += kAppendUnroll * lanes) {
+        if (h0 != lane) load(h0, nkv, kv_at);
+#pragma unroll
+        for (int i = 0; i < kAppendUnroll; ++i) {
+            const int h = h0 + i * lanes;
+            if (h < nkv) {
+                T *dst = (h < p.Hkv ? ap.k_cache + h * D : ap.v_cache + (h - p.Hkv) * D) + at + a;
+                if (turn && h < p.Hkv) rope_rotate<T, V, HALF>(u[i], w[i], f);
+                *reinterpret_cast<W *>(dst) = u[i];
+                if (b >= 0) *reinterpret_cast<W *>(dst + d) = w[i];
             }
         }
     }
-}
-
-// Tokens per block: enough (token, head, group) items for every thread to
-// have kUnroll of them in flight at least once, fewer where the blocks would
-// not cover the SMs, and no more factors than shared memory is set aside for.
-int tokens_per_block(long long n_tok, int heads, int groups, int n) {
-    const long long want = std::max(1, 2 * kUnroll * kThreads / (heads * groups));
-    const long long cover = std::max(1ll, n_tok / (2 * 148));
-    return (int)std::max(1ll, std::min({want, cover, (long long)(kMaxFactors / std::max(1, n))}));
 }
 
 // The widest access, in elements, that divides the pairs and the copied rest
@@ -211,34 +232,27 @@ int access_width(int size, int n, int D, uintptr_t bits) {
 template <typename T, int V>
 cudaError_t launch_rope(const attn_rope_s &r, const void *x, long long xs, long long n_tok, int H, const int32_t *pos,
                         long long ps, bool grad, void *out, long long os, cudaStream_t s) {
-    const int n = r.tab.n, groups = rope_groups(n, r.D, V), tpb = tokens_per_block(n_tok, H, groups, n);
-    const long long blocks = (n_tok + tpb - 1) / tpb;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)tpb * n * sizeof(float2);
-    auto *xi = static_cast<const T *>(x);
-    auto *oi = static_cast<T *>(out);
-    const float sign = grad ? -1.f : 1.f;
-    if (r.layout == ATTN_ROPE_HALF)
-        rope_kernel<T, V, true><<<(unsigned)blocks, kThreads, smem, s>>>(r.tab, xi, xs, n_tok, H, r.D, pos, ps, sign,
-                                                                          oi, os, tpb, groups);
-    else
-        rope_kernel<T, V, false><<<(unsigned)blocks, kThreads, smem, s>>>(r.tab, xi, xs, n_tok, H, r.D, pos, ps, sign,
-                                                                           oi, os, tpb, groups);
+    const Shape sh = shape_of(n_tok, H, rope_groups(r.tab.n, r.D, V), r.tab.n, kMaxHeads);
+    if (sh.blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    const size_t smem = (size_t)sh.tokens * r.tab.n * sizeof(float2);
+    auto *fn = r.layout == ATTN_ROPE_HALF ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
+    fn<<<(unsigned)sh.blocks, sh.threads, smem, s>>>(r.tab, static_cast<const T *>(x), xs, n_tok, H, r.D, pos, ps,
+                                                     grad ? -1.f : 1.f, static_cast<T *>(out), os, sh.groups, sh.lanes,
+                                                     sh.tokens);
     return cudaGetLastError();
 }
 
 template <int V>
 cudaError_t launch_append(const RopeTable &tab, bool half, const Params &p, Append ap, cudaStream_t s) {
-    const int heads = (ap.q_out ? p.Hq : 0) + 2 * p.Hkv;
-    ap.groups = rope_groups(tab.n, p.D, V);
-    ap.tpb = tokens_per_block(ap.n_tok, heads, ap.groups, std::max(tab.n, 64));
-    const long long blocks = (ap.n_tok + ap.tpb - 1) / ap.tpb;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)ap.tpb * (tab.n * sizeof(float2) + sizeof(long long) + sizeof(int));
-    if (half)
-        append_kernel<V, true><<<(unsigned)blocks, kThreads, smem, s>>>(tab, p, ap);
-    else
-        append_kernel<V, false><<<(unsigned)blocks, kThreads, smem, s>>>(tab, p, ap);
+    const Shape sh = shape_of(ap.n_tok, (ap.q_out ? p.Hq : 0) + 2 * p.Hkv, rope_groups(tab.n, p.D, V), tab.n,
+                              kAppendHeads);
+    if (sh.blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    ap.groups = sh.groups;
+    ap.lanes = sh.lanes;
+    ap.tokens = sh.tokens;
+    const size_t smem = (size_t)sh.tokens * (tab.n * sizeof(float2) + sizeof(long long) + sizeof(int2));
+    auto *fn = half ? append_kernel<V, true> : append_kernel<V, false>;
+    fn<<<(unsigned)sh.blocks, sh.threads, smem, s>>>(tab, p, ap);
     return cudaGetLastError();
 }
 

@@ -71,19 +71,58 @@ __host__ __device__ __forceinline__ int rope_groups(int n, int D, int V) {
     return n / V + (D - 2 * n + 2 * V - 1) / (2 * V);
 }
 
+// two 16-bit elements of a word
+template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w);
+template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <typename T> __device__ __forceinline__ uint32_t pack2(float x, float y);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, float y) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// one pair turned by c = (cos, sin)
+__device__ __forceinline__ float2 turn_pair(float u, float w, float2 c) {
+    return make_float2(u * c.x - w * c.y, u * c.y + w * c.x);
+}
+
 // rotate the V pairs held in (x, y) by the factors cs[0 .. V)
 template <typename T, int V, bool HALF>
 __device__ __forceinline__ void rope_rotate(Vec<T, V> &x, Vec<T, V> &y, const float2 *cs) {
-    T *p[2] = {x.e, y.e};
+    if constexpr (sizeof(T) == 2 && V > 1) {
+        uint32_t *xw = reinterpret_cast<uint32_t *>(&x), *yw = reinterpret_cast<uint32_t *>(&y);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        // the pair's two elements: i of x and i of y, or 2 i and 2 i + 1 of x then y
-        T &u = HALF ? p[0][i] : p[(2 * i) / V][(2 * i) % V];
-        T &w = HALF ? p[1][i] : p[(2 * i + 1) / V][(2 * i + 1) % V];
-        const float2 c = cs[i];
-        const float fu = to_f32(u), fw = to_f32(w);
-        u = from_f32<T>(fu * c.x - fw * c.y);
-        w = from_f32<T>(fu * c.y + fw * c.x);
+        for (int k = 0; k < V / 2; ++k) {
+            const float2 a = unpack2<T>(xw[k]), b = unpack2<T>(yw[k]);
+            if constexpr (HALF) {             // words of two firsts and of two seconds
+                const float2 p = turn_pair(a.x, b.x, cs[2 * k]), q = turn_pair(a.y, b.y, cs[2 * k + 1]);
+                xw[k] = pack2<T>(p.x, q.x);
+                yw[k] = pack2<T>(p.y, q.y);
+            } else {                          // words of one pair
+                const float2 p = turn_pair(a.x, a.y, cs[k]), q = turn_pair(b.x, b.y, cs[V / 2 + k]);
+                xw[k] = pack2<T>(p.x, p.y);
+                yw[k] = pack2<T>(q.x, q.y);
+            }
+        }
+    } else {
+        T *p[2] = {x.e, y.e};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            // the pair's two elements: i of x and i of y, or 2 i and 2 i + 1 of x then y
+            T &u = HALF ? p[0][i] : p[(2 * i) / V][(2 * i) % V];
+            T &w = HALF ? p[1][i] : p[(2 * i + 1) / V][(2 * i + 1) % V];
+            const float2 r = turn_pair(to_f32(u), to_f32(w), cs[i]);
+            u = from_f32<T>(r.x);
+            w = from_f32<T>(r.y);
+        }
     }
 }
 
