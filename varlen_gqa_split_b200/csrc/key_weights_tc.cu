@@ -18,10 +18,13 @@
 // parts, 256 sums each, are added in block order by whichever block finishes
 // last.  Decode has one row tile per item: no cuts, K streams through.
 //
-// Warps: 0-7 epilogue (warp w: sub-tile w / 4, lanes 32 (w mod 4)); 8 issues
-// the MMAs; 9 loads K and Q by TMA (128-byte swizzle, mbarrier rings); 10
-// stages -lse log2 e of each row tile.  Every wait is bounded, as in the
-// attention kernels.
+// Warps: 0-15 epilogue (warp w: sub-tile w / 4 mod 2, lanes 32 (w mod 4), and
+// of the columns, where there are 64 or more, half w / 8: four warps a
+// scheduler hide one another's latencies; at the end of an item the first
+// half adds the second's sums).  16 issues the MMAs, one row tile ahead of the
+// epilogue (two buffers of S); 17 loads K and Q by TMA (128-byte swizzle,
+// mbarrier rings); 18 stages -lse log2 e of each row tile.  Every wait is
+// bounded, as in the attention kernels.
 #include <algorithm>
 
 #include "common.cuh"
@@ -35,10 +38,10 @@ namespace {
 
 constexpr int kSubKeys = 128;             // keys per sub-tile (MMA M)
 constexpr int kItemKeys = 256;
-constexpr int kEpiWarps = 8;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kLseWarp = 10;
-constexpr int kThreads = 352;
-constexpr int kLseStages = 4;
+constexpr int kHalfWarps = 8;             // epilogue warps of a half of the columns
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kLseWarp = 18;
+constexpr int kThreads = 608;
+constexpr int kSumSlots = 4;              // sums on their way from half to half (at most 3 are)
 constexpr int kMaxStages = 8;
 constexpr size_t kMinSmem = 120 * 1024;   // one block per SM: tensor memory is never waited for
 
@@ -47,9 +50,11 @@ struct Layout {
     static constexpr int kHalves = D / 64;
     static constexpr int kSub = kSubKeys * D * 2;             // one sub-tile of K
     static constexpr int kQ = N * D * 2;                      // one row tile of Q
-    // ring depths: 200 KB in all; K first where N is small (decode streams
-    // K), at least two items' worth of K otherwise
-    static constexpr int kQStages = N == 128 ? 2 : 4;
+    static constexpr int kColHalves = N >= 64 ? 2 : 1;          // halves of the columns
+    // ring depths: 200 KB in all, K in what Q leaves.  A row tile of 128 x 128
+    // takes 1.3 us from its slot's release to its arrival, more than the
+    // product of one (0.6 us): three of them in flight, and 1.5 items of K
+    static constexpr int kQStages = kQ == 32768 ? 3 : 4;
     static constexpr int kKStages = (200 * 1024 - kQStages * kQ) / kSub < kMaxStages
                                         ? (200 * 1024 - kQStages * kQ) / kSub
                                         : kMaxStages;
@@ -203,18 +208,19 @@ struct Walker {
 
 // ------------------------------------------------------------ kernel
 
-// sum over 32 (or 16) columns of 2^(s scale + nl); MASKED: only those in `vis`
-template <int W, bool MASKED>
-__device__ __forceinline__ void add_columns(const uint32_t (&v)[W], const float *nl, float scale, uint32_t vis,
+// sum over 16 columns of 2^(s scale + nl); MASKED: only those in `vis`.  Taking
+// some of the exponentials on the FMA pipe (a polynomial) was measured and
+// lost: 1 of 8 pairs 1.72 ms where none takes 1.73, 3 of 8 1.90.
+template <bool MASKED>
+__device__ __forceinline__ void add_columns(const uint32_t (&v)[16], const float *nl, float2 scale, uint32_t vis,
                                             float2 (&acc)[4]) {
-    const float2 sc = make_float2(scale, scale);
 #pragma unroll
-    for (int i = 0; i < W; i += 4) {
+    for (int i = 0; i < 16; i += 4) {
         const float4 l = *reinterpret_cast<const float4 *>(nl + i);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int c = i + 2 * h;
-            const float2 t = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc,
+            const float2 t = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), scale,
                                    h ? make_float2(l.z, l.w) : make_float2(l.x, l.y));
             float2 e = make_float2(ex2(t.x), ex2(t.y));
             if (MASKED) {
@@ -235,11 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *ring_k = smem, *ring_q = ring_k + KS * L::kSub;
-    float *nl = reinterpret_cast<float *>(ring_q + QS * L::kQ);            // [kLseStages][N]
-    uint64_t *k_full = reinterpret_cast<uint64_t *>(nl + kLseStages * N), *k_empty = k_full + KS;
+    float *nl = reinterpret_cast<float *>(ring_q + QS * L::kQ);            // [2][N]
+    float *sums = nl + 2 * N;                                              // [kSumSlots][kItemKeys]
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(sums + kSumSlots * kItemKeys), *k_empty = k_full + KS;
     uint64_t *q_full = k_empty + KS, *q_empty = q_full + QS;
-    uint64_t *l_full = q_empty + QS, *l_empty = l_full + kLseStages;
-    uint64_t *s_full = l_empty + kLseStages, *s_free = s_full + 2, *drain = s_free + 2;
+    // [buffer]: scores and normalisers there; scores read; normalisers read
+    uint64_t *s_full = q_empty + QS, *s_free = s_full + 2, *l_empty = s_free + 2;
+    uint64_t *x_full = l_empty + 2, *drain = x_full + kSumSlots;
     long long *scan = reinterpret_cast<long long *>(drain + 1);            // [kThreads / 32]
     long long *found = scan + kThreads / 32;                               // [2]
     volatile int *stop = reinterpret_cast<volatile int *>(found + 2);
@@ -255,14 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
         }
-        for (int i = 0; i < kLseStages; ++i) {
-            mbar_init(&l_full[i], 1);
-            mbar_init(&l_empty[i], kEpiWarps);
-        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&s_free[i], kEpiWarps);
+            mbar_init(&s_full[i], 2);     // the MMA issuer's commit and the normalisers' warp
+            mbar_init(&s_free[i], L::kColHalves * kHalfWarps);
+            mbar_init(&l_empty[i], L::kColHalves * kHalfWarps);
         }
+        for (int i = 0; i < kSumSlots; ++i) mbar_init(&x_full[i], kHalfWarps);
         mbar_init(drain, 1);
         *stop = 0;
         fence_barrier_init();
@@ -372,62 +378,84 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
     } else if (has_work && warp == kMmaWarp) {
 
         // ------------------------------------------------------ MMA issue
-        if (lane == 0) {
-            constexpr uint32_t kId = tc::idesc_bf16_f32(kSubKeys, N, false);
-            const uint32_t k0 = smem_u32(ring_k), q0 = smem_u32(ring_q);
-            int ks = 0, qs = 0, j = 0;
-            uint32_t kph = 0, qph = 0;
-            bool ok = true;
-            Walker it;
-            it.init(p, sh);
-            do {
-                if (it.R == 0) continue;
-                const int nsub = it.sub_key(1) >= 0 ? 2 : 1;
-                int slot[2];
-                for (int u = 0; u < nsub && ok; ++u) {
-                    slot[u] = ks;
-                    ok = wait_bar(&k_full[ks], kph, stop, p);
-                    if (++ks == KS) {
-                        ks = 0;
-                        kph ^= 1;
-                    }
+        // the whole warp goes along, with values that are the same in all of
+        // its lanes, and one elected lane issues
+        constexpr uint32_t kId = tc::idesc_bf16_f32(kSubKeys, N, false);
+        auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+            return __all_sync(0xffffffffu, wait_bar(bar, parity, stop, p));
+        };
+        const uint32_t tm = uniform(tmem);
+        const uint64_t k_desc = tc::smem_desc_sw128(uniform(smem_u32(ring_k)), 16, 1024);
+        const uint64_t q_desc = tc::smem_desc_sw128(uniform(smem_u32(ring_q)), 16, 1024);
+        uint32_t ks = 0, qs = 0, j = 0, kph = 0, qph = 0;
+        bool ok = true, ready = false;       // ready: the next row tile's barriers were seen complete
+        Walker it;
+        it.init(p, sh);
+        do {
+            if (it.R == 0) continue;
+            const uint32_t nsub = uniform(it.sub_key(1) >= 0 ? 2 : 1), n = uniform(it.r1 - it.r0);
+            const uint32_t slot0 = ks, slot1 = ks + 1 == KS ? 0 : ks + 1;
+            for (uint32_t u = 0; u < nsub && ok; ++u) {
+                ok = wait_all(&k_full[ks], kph);
+                if (++ks == KS) {
+                    ks = 0;
+                    kph ^= 1;
                 }
-                for (int r = it.r0; r < it.r1 && ok; ++r, ++j) {
-                    const int buf = j & 1;
-                    if (!(ok = wait_bar(&q_full[qs], qph, stop, p))) break;
-                    if (j >= 2 && !(ok = wait_bar(&s_free[buf], ((j >> 1) - 1) & 1, stop, p))) break;
-                    tc::fence_after_sync();
-                    const uint64_t bd = tc::smem_desc_sw128(q0 + qs * L::kQ, 16, 1024);
-                    for (int u = 0; u < nsub; ++u) {
-                        const uint64_t ad = tc::smem_desc_sw128(k0 + slot[u] * L::kSub, 16, 1024);
+            }
+            const uint64_t a0 = k_desc + (slot0 * L::kSub >> 4), a1 = k_desc + (slot1 * L::kSub >> 4);
+            for (uint32_t r = 0; r < n && ok; ++r, ++j) {
+                const uint32_t buf = j & 1;
+                if (!ready) {
+                    if (!(ok = wait_all(&q_full[qs], qph))) break;
+                    if (j >= 2 && !(ok = wait_all(&s_free[buf], ((j >> 1) - 1) & 1))) break;
+                }
+                tc::fence_after_sync();
+                const uint64_t bd = q_desc + (qs * L::kQ >> 4);
+                const uint32_t d = tm + buf * 2 * N, qe = smem_u32(&q_empty[qs]), sf = smem_u32(&s_full[buf]);
+                if (++qs == QS) {
+                    qs = 0;
+                    qph ^= 1;
+                }
+                // the two sub-tiles' products take turns, so that no product
+                // waits for the one before it
+                auto issue = [&](int k_from, int k_to) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const int hf = kk >> 2, cc = (kk & 3) * 32;
-                            tc::mma_bf16_ss(tmem + (buf * 2 + u) * N, ad + ((hf * kSubKeys * 128 + cc) >> 4),
-                                            bd + ((hf * N * 128 + cc) >> 4), kId, kk > 0);
-                        }
+                    for (int kk = k_from; kk < k_to; ++kk) {
+                        const uint32_t ao = ((kk >> 2) * kSubKeys * 128 + (kk & 3) * 32) >> 4;
+                        const uint32_t bo = ((kk >> 2) * N * 128 + (kk & 3) * 32) >> 4;
+                        tc::mma_bf16_ss_elected(d, a0 + ao, bd + bo, kId, kk > 0);
+                        if (nsub == 2) tc::mma_bf16_ss_elected(d + N, a1 + ao, bd + bo, kId, kk > 0);
                     }
-                    tc::commit(smem_u32(&q_empty[qs]));
-                    tc::commit(smem_u32(&s_full[buf]));
-                    if (++qs == QS) {
-                        qs = 0;
-                        qph ^= 1;
-                    }
+                };
+                if (tc::elect_one()) issue(0, D / 32);
+                __syncwarp();
+                // what the next row tile needs is looked at while these run
+                ready = __all_sync(0xffffffffu, mbar_test_wait(&q_full[qs], qph) &&
+                                                    (j == 0 || mbar_test_wait(&s_free[buf ^ 1], (((j + 1) >> 1) - 1) & 1)));
+                if (tc::elect_one()) {
+                    issue(D / 32, D / 16);
+                    tc::commit(sf);
+                    tc::commit(qe);
                 }
-                if (ok)
-                    for (int u = 0; u < nsub; ++u) tc::commit(smem_u32(&k_empty[slot[u]]));
-            } while (ok && it.next(p));
-            if (!ok) *stop = 1;
-            // nothing this thread issued may still run when the memory is freed
-            tc::commit(smem_u32(drain));
-            mbar_wait(drain, 0);
-        }
+                __syncwarp();
+            }
+            if (ok && tc::elect_one()) {
+                tc::commit(smem_u32(&k_empty[slot0]));
+                if (nsub == 2) tc::commit(smem_u32(&k_empty[slot1]));
+            }
+            __syncwarp();
+        } while (ok && it.next(p));
+        if (!ok) *stop = 1;
+        // nothing that was issued may still run when the memory is freed
+        if (tc::elect_one()) tc::commit(smem_u32(drain));
+        __syncwarp();
+        mbar_wait(drain, 0);
         __syncwarp();
     } else if (has_work && warp == kLseWarp) {
 
         // ------------------------------------------------------ normalisers
-        int ls = 0, j = 0;
-        uint32_t lph = 0;
+        int j = 0;
         bool ok = true;
         constexpr int kPer = (N + 31) / 32;
         int tok[kPer], off[kPer];            // column lane + 32 i: its token in the tile, its offset in lse
@@ -447,130 +475,133 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 float v[kPer];
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) v[i] = tok[i] >= 0 && t0 + tok[i] >= 0 ? __ldg(src + off[i]) : -INFINITY;
-                if (j >= kLseStages &&
-                    !(ok = __all_sync(0xffffffffu, wait_bar(&l_empty[ls], lph ^ 1, stop, p))))
+                const int buf = j & 1;
+                if (j >= 2 &&
+                    !(ok = __all_sync(0xffffffffu, wait_bar(&l_empty[buf], ((j >> 1) - 1) & 1, stop, p))))
                     break;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i)
                     if (lane + 32 * i < N)   // a row that saw nothing (lse = -inf) weighs nothing
-                        nl[ls * N + lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kLog2e;
+                        nl[buf * N + lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kLog2e;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&l_full[ls]);
-                if (++ls == kLseStages) {
-                    ls = 0;
-                    lph ^= 1;
-                }
+                if (lane == 0) mbar_arrive(&s_full[buf]);
             }
         } while (ok && it.next(p));
         if (!ok) *stop = 1;
-    } else if (has_work && warp < kEpiWarps) {
+    } else if (has_work && warp < L::kColHalves * kHalfWarps) {
 
         // ------------------------------------------------------ exponentials and sums
-        const int u = warp >> 2, lane_key = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const float scale = p.scale_log2;
+        constexpr int kCols = N / L::kColHalves;                   // this warp's columns
+        const int half = warp / kHalfWarps, wi = warp % kHalfWarps;
+        const int u = wi >> 2, lane_key = (wi & 3) * 32 + lane, x = u * kSubKeys + lane_key;
+        const int col0 = half * kCols;
+        const uint32_t ts = tmem + ((uint32_t)((wi & 3) * 32) << 16) + u * N + col0;
+        const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+        const bool writes = half == 0;
         auto wwait = [&](uint64_t *bar, uint32_t parity) -> bool {
             return __all_sync(0xffffffffu, wait_bar(bar, parity, stop, p));
         };
-        int ls = 0, j = 0;
-        uint32_t lph = 0;
-        bool ok = true;
+        int j = 0, joined = 0;                                   // row tiles and items so far
+        bool ok = true, ready = false;                           // ready: the next row tile's scores were seen
         Walker it;
         it.init(p, sh);
         do {
+            const int n = it.R > 0 ? it.r1 - it.r0 : 0;
+            if (n == 0 && !writes) continue;
             const int j0 = it.sub_key(u);
             const bool live = j0 >= 0;
             const int key = (PAGED ? j0 : min(j0, it.s.Lk - kSubKeys)) + lane_key;
-            const bool mine = live && key >= j0 && key < it.s.Lk;
+            const bool mine = writes && live && key >= j0 && key < it.s.Lk;
             const int old = it.s.Lk - it.s.Lq;                   // keys below it were there before
             const long long at = ((long long)it.b * p.Hkv + it.hk) * kw.ld + key;
-            const bool whole = it.r0 == 0 && it.r1 == it.w;
             // what the key had gathered, on its way while the products run
             float before = 0.f;
             if (mine && kw.w_in && kw.decay != 0.f && key < old) before = __ldcg(kw.w_in + at);
             float total = 0.f, carry = 0.f;
-            if (it.R > 0) {
-                for (int r = it.r0; r < it.r1; ++r, ++j) {
-                    const int buf = j & 1;
-                    if (!(ok = wwait(&l_full[ls], lph)) || !(ok = wwait(&s_full[buf], (j >> 1) & 1))) break;
-                    tc::fence_after_sync();
+            for (int i = 0; i < n; ++i, ++j) {
+                const int buf = j & 1;
+                if (!__all_sync(0xffffffffu, ready) && !(ok = wwait(&s_full[buf], (j >> 1) & 1))) break;
+                tc::fence_after_sync();
+                const int t0 = it.s.Lq - (it.r0 + i + 1) * QT;
+                // all columns see every key of the sub-tile
+                const bool clear = t0 >= 0 && j0 + kSubKeys - 1 - old - t0 <= 0 && ncols == N;
+                const uint32_t tb = ts + buf * 2 * N;
+                const float *n0 = nl + buf * N + col0;
+                float2 acc[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int ch = 0; ch < kCols / 16; ++ch) {
+                    uint32_t v[16];
                     if (live) {
-                        const int t0 = it.s.Lq - (r + 1) * QT;
-                        // columns [first, ncols) see this key; all of them see every
-                        // key of the sub-tile where `clear`
-                        const int first = max(0, max(-t0, key - old - t0)) * G;
-                        const bool clear = t0 >= 0 && j0 + kSubKeys - 1 - old - t0 <= 0 && ncols == N;
-                        const uint32_t ts = tmem + lane_base + (buf * 2 + u) * N;
-                        const float *n0 = nl + ls * N;
-                        float2 acc[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
-                        if constexpr (N == 16) {
-                            uint32_t v[16];
-                            tc::ld_32x32b_x16(ts, v);
-                            tc::wait_ld();
-                            const uint32_t vis = first >= 16 ? 0u : (0xffffffffu << first) & ((1u << ncols) - 1u);
-                            if (clear) add_columns<16, false>(v, n0, scale, 0, acc);
-                            else add_columns<16, true>(v, n0, scale, vis, acc);
+                        tc::ld_32x32b_x16(tb + ch * 16, v);
+                        tc::wait_ld();
+                    }
+                    if (ch + 1 == kCols / 16) {
+                        // everything read: the buffer is free, and the next one
+                        // may be there already
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s_free[buf]);
+                        ready = mbar_test_wait(&s_full[buf ^ 1], ((j + 1) >> 1) & 1);
+                    }
+                    if (live) {
+                        if (clear) {
+                            add_columns<false>(v, n0 + ch * 16, scale, 0, acc);
                         } else {
-                            uint32_t v[2][32];
-                            tc::ld_32x32b_x32(ts, v[0]);
-#pragma unroll
-                            for (int ch = 0; ch < N / 32; ++ch) {
-                                tc::wait_ld();
-                                if (ch + 1 < N / 32) tc::ld_32x32b_x32(ts + (ch + 1) * 32, v[(ch + 1) & 1]);
-                                if (clear) {
-                                    add_columns<32, false>(v[ch & 1], n0 + ch * 32, scale, 0, acc);
-                                } else {
-                                    const int lo = min(32, max(0, first - ch * 32)), hi = min(32, max(0, ncols - ch * 32));
-                                    const uint32_t vis = (uint32_t)((1ull << hi) - 1ull) & (uint32_t)~((1ull << lo) - 1ull);
-                                    add_columns<32, true>(v[ch & 1], n0 + ch * 32, scale, vis, acc);
-                                }
-                            }
+                            // columns [first, ncols) see this key
+                            const int c0 = col0 + ch * 16, first = max(0, max(-t0, key - old - t0)) * G;
+                            const int lo = min(16, max(0, first - c0)), hi = min(16, max(0, ncols - c0));
+                            add_columns<true>(v, n0 + ch * 16, scale, (1u << hi) - (1u << min(lo, hi)), acc);
                         }
-                        const float2 s2 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-                        // compensated: many row tiles may add up
-                        const float y = (s2.x + s2.y) - carry, t = total + y;
-                        carry = (t - total) - y;
-                        total = t;
-                    }
-                    tc::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&s_free[buf]);
-                        mbar_arrive(&l_empty[ls]);
-                    }
-                    if (++ls == kLseStages) {
-                        ls = 0;
-                        lph ^= 1;
                     }
                 }
-                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&l_empty[buf]);
+                const float2 s2 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+                // compensated: many row tiles may add up
+                const float y = (s2.x + s2.y) - carry, t = total + y;
+                carry = (t - total) - y;
+                total = t;
             }
-            bool write = true;
-            if (!whole && live) {
-                // this part's sums; of the item's blocks, the one whose warp is
-                // the last to finish adds them all up in block order (the first
-                // part of an item is its block's last: slot 2 c + 1, every other
-                // part slot 2 c).  Each warp counts for its own 32 keys, so no
-                // barrier joins warps of which one may have given up.
+            if (!ok) break;
+            if (L::kColHalves == 2 && n > 0) {
+                const int slot = joined % kSumSlots;
+                float *xs = sums + slot * kItemKeys + x;
+                if (!writes) {
+                    *xs = total;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&x_full[slot]);
+                } else {
+                    if (!(ok = wwait(&x_full[slot], (joined / kSumSlots) & 1))) break;
+                    total += *xs;
+                }
+                ++joined;
+            }
+            if (!writes) continue;
+            bool all = true;
+            if (live && (it.r0 > 0 || it.r1 < it.w)) {
+                // a part of the item's sums; of the item's blocks, the one whose
+                // warp is the last to finish adds them all up in block order (the
+                // first part of an item is its block's last: slot 2 c + 1, every
+                // other part slot 2 c).  Each warp counts for its own 32 keys, so
+                // no barrier joins warps of which one may have given up.
                 const int c0 = block_of(it.P, sh), c1 = block_of(it.P + it.w - 1, sh), c = (int)blockIdx.x;
-                const int x = u * kSubKeys + lane_key;
-                uint32_t *ticket = kw.ticket + c0 * kEpiWarps + warp;
+                uint32_t *ticket = kw.ticket + c0 * kHalfWarps + wi;
                 __stcg(kw.part + (long long)(2 * c + (c == c0)) * kItemKeys + x, total);
                 __threadfence();
                 __syncwarp();
                 uint32_t done = 0;
                 if (lane == 0) done = atomicAdd(ticket, 1u);
-                write = __shfl_sync(0xffffffffu, done, 0) == (uint32_t)(c1 - c0);
-                if (write) {
+                all = __shfl_sync(0xffffffffu, done, 0) == (uint32_t)(c1 - c0);
+                if (all) {
                     __threadfence();
                     total = 0.f;
                     for (int i = c0; i <= c1; ++i) total += __ldcg(kw.part + (long long)(2 * i + (i == c0)) * kItemKeys + x);
                     if (lane == 0) *ticket = 0u;
                 }
             }
-            if (write && mine) {
+            if (all && mine) {
                 kw.w_out[at] = kw.decay * before + total;
                 if (kw.born && key >= old) kw.born[at] = __ldg(kw.seen + it.b) - (it.s.Lk - key);
             }
@@ -590,9 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
 template <int D, int N>
 constexpr size_t smem_need() {
     using L = Layout<D, N>;
-    // alignment slack, rings, normalisers, barriers, scan, found, flags
-    const size_t need = 1024 + (size_t)L::kKStages * L::kSub + (size_t)L::kQStages * L::kQ + kLseStages * N * 4 +
-                        (2 * L::kKStages + 2 * L::kQStages + 2 * kLseStages + 5) * 8 + (kThreads / 32 + 2) * 8 + 16;
+    // alignment slack, rings, normalisers, sums, barriers, scan, found, flags
+    const size_t need = 1024 + (size_t)L::kKStages * L::kSub + (size_t)L::kQStages * L::kQ + 2 * N * 4 +
+                        kSumSlots * kItemKeys * 4 + (2 * L::kKStages + 2 * L::kQStages + kSumSlots + 7) * 8 + (kThreads / 32 + 2) * 8 + 16;
     return need > kMinSmem ? need : kMinSmem;
 }
 
@@ -619,7 +650,7 @@ void pick(int D, int n, bool paged, Kernel &fn, size_t &smem) {
 int key_weights_columns(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 int key_weights_part_floats() { return 2 * kItemKeys; }
-int key_weights_tickets() { return kEpiWarps; }
+int key_weights_tickets() { return kHalfWarps; }
 
 cudaError_t key_weights_tc_prepare(int D, int columns) {
     for (bool paged : {false, true}) {
