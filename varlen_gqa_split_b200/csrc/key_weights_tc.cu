@@ -51,10 +51,9 @@ struct Layout {
     static constexpr int kSub = kSubKeys * D * 2;             // one sub-tile of K
     static constexpr int kQ = N * D * 2;                      // one row tile of Q
     static constexpr int kColHalves = N >= 64 ? 2 : 1;          // halves of the columns
-    // ring depths: 200 KB in all, K in what Q leaves.  A row tile of 128 x 128
-    // takes 1.3 us from its slot's release to its arrival, more than the
-    // product of one (0.6 us): three of them in flight, and 1.5 items of K
-    static constexpr int kQStages = kQ == 32768 ? 3 : 4;
+    // ring depths: 200 KB in all, K in what Q leaves (with the largest tiles two
+    // row tiles and two items of K; three and one and a half took as long)
+    static constexpr int kQStages = kQ == 32768 ? 2 : 4;
     static constexpr int kKStages = (200 * 1024 - kQStages * kQ) / kSub < kMaxStages
                                         ? (200 * 1024 - kQStages * kQ) / kSub
                                         : kMaxStages;
@@ -213,7 +212,7 @@ struct Walker {
 // lost: 1 of 8 pairs 1.72 ms where none takes 1.73, 3 of 8 1.90.
 template <bool MASKED>
 __device__ __forceinline__ void add_columns(const uint32_t (&v)[16], const float *nl, float2 scale, uint32_t vis,
-                                            float2 (&acc)[4]) {
+                                            float2 (&acc)[2]) {
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
         const float4 l = *reinterpret_cast<const float4 *>(nl + i);
@@ -227,7 +226,7 @@ __device__ __forceinline__ void add_columns(const uint32_t (&v)[16], const float
                 if (!(vis >> c & 1u)) e.x = 0.f;
                 if (!(vis >> (c + 1) & 1u)) e.y = 0.f;
             }
-            acc[(c >> 1) & 3] = fadd2(acc[(c >> 1) & 3], e);
+            acc[h] = fadd2(acc[h], e);
         }
     }
 }
@@ -523,17 +522,19 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 if (!__all_sync(0xffffffffu, ready) && !(ok = wwait(&s_full[buf], (j >> 1) & 1))) break;
                 tc::fence_after_sync();
                 const int t0 = it.s.Lq - (it.r0 + i + 1) * QT;
-                // all columns see every key of the sub-tile
-                const bool clear = t0 >= 0 && j0 + kSubKeys - 1 - old - t0 <= 0 && ncols == N;
+                // every column from `all_from` on sees all of the sub-tile's keys, none
+                // before `any_from` sees any of them
+                const int any_from = max(0, max(-t0, j0 - old - t0)) * G;
+                const int all_from = max(0, max(-t0, j0 + kSubKeys - 1 - old - t0)) * G;
                 const uint32_t tb = ts + buf * 2 * N;
                 const float *n0 = nl + buf * N + col0;
-                float2 acc[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int ch = 0; ch < kCols / 16; ++ch) {
+                    const int c0 = col0 + ch * 16;
+                    const bool some = live && c0 + 16 > any_from && c0 < ncols;
                     uint32_t v[16];
-                    if (live) {
+                    if (some) {
                         tc::ld_32x32b_x16(tb + ch * 16, v);
                         tc::wait_ld();
                     }
@@ -545,20 +546,20 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                         if (lane == 0) mbar_arrive(&s_free[buf]);
                         ready = mbar_test_wait(&s_full[buf ^ 1], ((j + 1) >> 1) & 1);
                     }
-                    if (live) {
-                        if (clear) {
+                    if (some) {
+                        if (c0 >= all_from && c0 + 16 <= ncols) {
                             add_columns<false>(v, n0 + ch * 16, scale, 0, acc);
                         } else {
                             // columns [first, ncols) see this key
-                            const int c0 = col0 + ch * 16, first = max(0, max(-t0, key - old - t0)) * G;
-                            const int lo = min(16, max(0, first - c0)), hi = min(16, max(0, ncols - c0));
+                            const int first = max(0, max(-t0, key - old - t0)) * G;
+                            const int lo = min(16, max(0, first - c0)), hi = min(16, ncols - c0);
                             add_columns<true>(v, n0 + ch * 16, scale, (1u << hi) - (1u << min(lo, hi)), acc);
                         }
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&l_empty[buf]);
-                const float2 s2 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+                const float2 s2 = fadd2(acc[0], acc[1]);
                 // compensated: many row tiles may add up
                 const float y = (s2.x + s2.y) - carry, t = total + y;
                 carry = (t - total) - y;
