@@ -50,7 +50,7 @@ extern "C" {
 #define ATTN_E_UNSUPPORTED (-2)   /* e.g. head dim not in {64, 128}           */
 #define ATTN_E_NULL (-3)          /* a required pointer is NULL               */
 #define ATTN_E_ALIGNMENT (-4)     /* a pointer breaks the alignment contract  */
-#define ATTN_E_BAD_PLAN (-5)      /* unknown or destroyed plan handle         */
+#define ATTN_E_BAD_PLAN (-5)      /* unknown or destroyed plan or rope handle */
 #define ATTN_E_CUDA (-6)          /* a CUDA runtime / driver call failed      */
 #define ATTN_E_NOMEM (-7)         /* device allocation failed                 */
 #define ATTN_E_DEVICE (-8)        /* current device is not the plan's device  */
@@ -414,7 +414,7 @@ typedef struct attn_rope_s *attn_rope_t;   /* opaque */
  */
 int attn_rope_create(attn_rope_t *out, int D, int n_pairs, int n_axes, const double *freq, const int32_t *axis,
                      int layout, float scale);
-void attn_rope_destroy(attn_rope_t rope);   /* NULL is ignored */
+void attn_rope_destroy(attn_rope_t rope);   /* NULL or an unknown handle is ignored */
 
 /*
  * attn_rope_apply -- rotate the heads of T tokens, asynchronous on `stream`,

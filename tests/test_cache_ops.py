@@ -45,7 +45,10 @@ def test_rope_create_nulls_and_destroy(L):
     rc, h = _create(L, D=256, n=128, axes=8)
     assert rc == OK and h.value
     L.attn_rope_destroy(h)
+    L.attn_rope_destroy(h)                                   # already gone, unknown, NULL: ignored
+    L.attn_rope_destroy(0x1234)
     L.attn_rope_destroy(None)
+    assert _apply(L, h) == BAD_PLAN and _apply(L, 0x1234) == BAD_PLAN
 
 
 def _apply(L, h, dtype=0, x=0x10000, xs=16, T=4, H=2, pos=0x900000, ps=4, grad=0, out=0x20000, os_=16):

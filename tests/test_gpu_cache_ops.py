@@ -446,6 +446,21 @@ def test_key_weights_minus_inf_lse_and_foreign_nans():
     assert out[1, :, :70].isnan().all()
 
 
+@pytest.mark.parametrize("Hq,Hkv,max_q,lq", [(8, 2, 40, 40), (8, 1, 1, 1), (16, 1, 8, 5), (136, 1, 3, 3)])
+def test_key_weights_skips_rows_without_a_normaliser(Hq, Hkv, max_q, lq):
+    """lse = -inf takes a row out whatever its query holds (NaN here), in tiles
+    that every row sees as in those that the mask cuts."""
+    D, lk = 64, 700
+    q, k = _bf16((lq, Hq, D), 1), _bf16((lk, Hkv, D), 2)
+    lse = _lse64(q, [k], np.array([lq]), np.array([lk]), Hq // Hkv)
+    lse[lq // 2:, ::3] = -math.inf
+    ref, tol = _weights64(q, [k], np.array([lq]), np.array([lk]), lse, Hq // Hkv, 1.0, None, Hkv, lk)
+    q[lse.isneginf()] = float("nan")
+    plan = Plan(1, lk, Hq, Hkv, D, max_q)
+    out = plan.key_weights(q, k, _cu([lq]), _cu([lk]), lse)
+    assert ((out.double() - ref).abs() <= tol).all()
+
+
 def test_key_weights_errors_are_reported_and_contained():
     B, Hq, Hkv, D, s_max = 3, 8, 2, 64, 100
     q, k = _bf16((9, Hq, D), 1), _bf16((300, Hkv, D), 2)
@@ -797,6 +812,41 @@ def test_serving_loop():
             at += n_new
         assert s.lens.cpu().tolist() == [len(s.ref[b][0]["born"]) for b in range(B)]
         assert s.seen.cpu().tolist() == s.total
+
+
+def test_first_calls_inside_a_capture():
+    """Nothing is set up by a first call: a fresh process may make it while
+    capturing (the plan was made before)."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from varlen_gqa_split_b200 import Plan, Rope, rope_table
+plan, rope = Plan(1, 64, 4, 2, 64, 2), Rope(64, *rope_table(32))
+x, k = (torch.ones(2, h, 64, dtype=torch.bfloat16, device='cuda') for h in (4, 2))
+out, q_out = torch.zeros_like(x), torch.zeros_like(x)
+pos = torch.tensor([[1, 2]], dtype=torch.int32, device='cuda')
+kc, vc = (torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16, device='cuda') for _ in range(2))
+bt = torch.arange(4, dtype=torch.int32, device='cuda')[None]
+cu, lse = torch.tensor([0, 2], dtype=torch.int32, device='cuda'), torch.zeros(2, 4, device='cuda')
+w, born = torch.zeros(1, 2, 64, device='cuda'), torch.zeros(1, 2, 64, dtype=torch.int32, device='cuda')
+seen, keep = (torch.tensor([n], dtype=torch.int32, device='cuda') for n in (2, 1))
+cu_new = torch.zeros_like(cu)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    rope.apply(x, pos, out)
+    plan.append_paged(k, k, kc, vc, bt, cu, cu, q=x, pos=pos, rope=rope, q_out=q_out)
+    plan.key_weights_paged(q_out, kc, bt, cu, cu, lse, out=w, seen=seen, born=born)
+    plan.evict_paged(w, born, seen, keep, kc, vc, bt, cu, cu_k_out=cu_new)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, q_out) and out.float().abs().sum() > 0 and cu_new.tolist() == [0, 1]
+assert plan.check_error() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120,
+                       cwd=W.__file__.rsplit("/", 1)[0])
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("max_q,Hq", [(1, 8), (12, 32)])

@@ -164,7 +164,7 @@ ATTN_EXPORT const char *attn_strerror(int code) {
     case ATTN_E_UNSUPPORTED: return "unsupported configuration (head dim must be 64 or 128)";
     case ATTN_E_NULL: return "a required pointer is NULL";
     case ATTN_E_ALIGNMENT: return "a pointer breaks the alignment contract (16 B tensors, 4 B cu/lse)";
-    case ATTN_E_BAD_PLAN: return "unknown or destroyed plan";
+    case ATTN_E_BAD_PLAN: return "unknown or destroyed plan or rope table";
     case ATTN_E_CUDA: return "a CUDA call failed";
     case ATTN_E_NOMEM: return "device allocation failed";
     case ATTN_E_DEVICE: return "current device differs from the plan's device";

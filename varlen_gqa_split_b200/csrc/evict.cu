@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int unit = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    dependent_start();
     if (unit == p.B_max * p.Hkv) {        // the extra cluster
         if (rank == 0) write_offsets(p, e, sh.scratch);
         return;
@@ -468,19 +469,8 @@ cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
     e.slice_words = slice_words(p.s_max, cs);
     const size_t fixed = sizeof(Head) + bits_bytes(p.s_max, cs), ranks = (size_t)e.slice_words * 32 * 4;
     e.cached = fixed + ranks <= (size_t)kMaxSmem ? e.slice_words * 32 : 0;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cs;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((p.B_max * p.Hkv + 1) * cs));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = fixed + (e.cached ? ranks : 0);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, p, e);
+    return launch_dependent(evict_kernel, dim3((unsigned)((p.B_max * p.Hkv + 1) * cs)), dim3(kThreads),
+                            fixed + (e.cached ? ranks : 0), stream, cs, p, e);
 }
 
 bool overlap(const void *a, const void *b, size_t na, size_t nb) {

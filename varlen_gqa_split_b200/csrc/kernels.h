@@ -9,6 +9,30 @@ namespace vgqa {
 
 struct Params;
 
+// A launch as a programmatic dependent of the work before it in the stream
+// (the kernel starts with dependent_start); in clusters of `cluster` blocks
+// where it is not zero.  Takes about 0.6 us off a small call that follows
+// another (rope of 64 tokens 3.45 -> 2.88 us).
+template <typename... A>
+cudaError_t launch_dependent(void (*fn)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
+                             const A &...args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 // CUDA-core split kernel (any row count), 16 query rows per block
 size_t simt_smem_bytes(int D);
 size_t simt_merge_capacity(int D);

@@ -222,9 +222,9 @@ __device__ __forceinline__ void add_columns(const uint32_t (&v)[16], const float
             const float2 t = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), scale,
                                    h ? make_float2(l.z, l.w) : make_float2(l.x, l.y));
             float2 e = make_float2(ex2(t.x), ex2(t.y));
-            if (MASKED) {
-                if (!(vis >> c & 1u)) e.x = 0.f;
-                if (!(vis >> (c + 1) & 1u)) e.y = 0.f;
+            if (MASKED) {                     // a row with lse = -inf counts for nothing, whatever its score
+                if (!(vis >> c & 1u) || (h ? l.z : l.x) == -INFINITY) e.x = 0.f;
+                if (!(vis >> (c + 1) & 1u) || (h ? l.w : l.y) == -INFINITY) e.y = 0.f;
             }
             acc[h] = fadd2(acc[h], e);
         }
@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
     long long *scan = reinterpret_cast<long long *>(drain + 1);            // [kThreads / 32]
     long long *found = scan + kThreads / 32;                               // [2]
     volatile int *stop = reinterpret_cast<volatile int *>(found + 2);
+    int *skips = reinterpret_cast<int *>(found + 2) + 2;                   // [2] the row tile has rows with lse = -inf
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(found + 2) + 1;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
         tc::tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
         tc::tmem_relinquish();
     }
+    dependent_start();
     Share sh;
     const bool has_work = block_share(p, tid, scan, found, sh);
     tc::fence_before_sync();
@@ -472,8 +474,14 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 const int t0 = it.s.Lq - (r + 1) * QT;                     // may be negative: those rows do not exist
                 const float *src = p.lse + ((long long)it.s.q0 + t0) * p.Hq + it.hk * G;
                 float v[kPer];
+                bool skip = false;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) v[i] = tok[i] >= 0 && t0 + tok[i] >= 0 ? __ldg(src + off[i]) : -INFINITY;
+                for (int i = 0; i < kPer; ++i) {
+                    const bool row = tok[i] >= 0 && t0 + tok[i] >= 0;
+                    v[i] = row ? __ldg(src + off[i]) : -INFINITY;
+                    skip |= row && v[i] == -INFINITY;
+                }
+                skip = __any_sync(0xffffffffu, skip);
                 const int buf = j & 1;
                 if (j >= 2 &&
                     !(ok = __all_sync(0xffffffffu, wait_bar(&l_empty[buf], ((j >> 1) - 1) & 1, stop, p))))
@@ -482,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 for (int i = 0; i < kPer; ++i)
                     if (lane + 32 * i < N)   // a row that saw nothing (lse = -inf) weighs nothing
                         nl[buf * N + lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kLog2e;
+                if (lane == 0) skips[buf] = skip;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_full[buf]);
             }
@@ -522,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 if (!__all_sync(0xffffffffu, ready) && !(ok = wwait(&s_full[buf], (j >> 1) & 1))) break;
                 tc::fence_after_sync();
                 const int t0 = it.s.Lq - (it.r0 + i + 1) * QT;
+                const bool skip = skips[buf] != 0;
                 // every column from `all_from` on sees all of the sub-tile's keys, none
                 // before `any_from` sees any of them
                 const int any_from = max(0, max(-t0, j0 - old - t0)) * G;
@@ -547,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                         ready = mbar_test_wait(&s_full[buf ^ 1], ((j + 1) >> 1) & 1);
                     }
                     if (some) {
-                        if (c0 >= all_from && c0 + 16 <= ncols) {
+                        if (c0 >= all_from && c0 + 16 <= ncols && !skip) {
                             add_columns<false>(v, n0 + ch * 16, scale, 0, acc);
                         } else {
                             // columns [first, ncols) see this key
@@ -669,8 +679,7 @@ cudaError_t launch_key_weights_tc(const Params &p, const KeyWeights &kw, const C
     Kernel fn;
     size_t smem;
     pick(p.D, columns, p.block_table != nullptr, fn, smem);
-    fn<<<ctas, kThreads, smem, stream>>>(tm_q, tm_k, p, kw);
-    return cudaGetLastError();
+    return launch_dependent(fn, dim3(ctas), dim3(kThreads), smem, stream, 0, tm_q, tm_k, p, kw);
 }
 
 }  // namespace vgqa

@@ -11,7 +11,9 @@
 // 16-byte loads and two 16-byte stores a head, several heads in flight.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 #include <new>
+#include <unordered_set>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -72,6 +74,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 const int32_t *__restrict__ pos, long long ps, float sign, T *out, long long os, int groups, int lanes,
                 int tokens) {
     extern __shared__ float2 cs[];
+    dependent_start();
     const int n = tab.n;
     const long long t0 = (long long)blockIdx.x * tokens;
     const int nt = (int)min((long long)tokens, n_tok - t0);
@@ -236,10 +239,9 @@ cudaError_t launch_rope(const attn_rope_s &r, const void *x, long long xs, long 
     if (sh.blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     const size_t smem = (size_t)sh.tokens * r.tab.n * sizeof(float2);
     auto *fn = r.layout == ATTN_ROPE_HALF ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
-    fn<<<(unsigned)sh.blocks, sh.threads, smem, s>>>(r.tab, static_cast<const T *>(x), xs, n_tok, H, r.D, pos, ps,
-                                                     grad ? -1.f : 1.f, static_cast<T *>(out), os, sh.groups, sh.lanes,
-                                                     sh.tokens);
-    return cudaGetLastError();
+    return launch_dependent(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, r.tab,
+                            static_cast<const T *>(x), xs, n_tok, H, r.D, pos, ps, grad ? -1.f : 1.f,
+                            static_cast<T *>(out), os, sh.groups, sh.lanes, sh.tokens);
 }
 
 template <int V>
@@ -252,8 +254,7 @@ cudaError_t launch_append(const RopeTable &tab, bool half, const Params &p, Appe
     ap.tokens = sh.tokens;
     const size_t smem = (size_t)sh.tokens * (tab.n * sizeof(float2) + sizeof(long long) + sizeof(int2));
     auto *fn = half ? append_kernel<V, true> : append_kernel<V, false>;
-    fn<<<(unsigned)sh.blocks, sh.threads, smem, s>>>(tab, p, ap);
-    return cudaGetLastError();
+    return launch_dependent(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, tab, p, ap);
 }
 
 }  // namespace
@@ -261,6 +262,18 @@ cudaError_t launch_append(const RopeTable &tab, bool half, const Params &p, Appe
 }  // namespace vgqa
 
 using namespace vgqa;
+
+namespace {
+
+std::mutex g_mu;
+std::unordered_set<attn_rope_s *> g_ropes;
+
+bool known(attn_rope_s *r) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    return g_ropes.count(r) != 0;
+}
+
+}  // namespace
 
 ATTN_EXPORT int attn_rope_create(attn_rope_t *out, int D, int n_pairs, int n_axes, const double *freq,
                                  const int32_t *axis, int layout, float scale) {
@@ -288,16 +301,30 @@ ATTN_EXPORT int attn_rope_create(attn_rope_t *out, int D, int n_pairs, int n_axe
         r->tab.turn[i] = f >= 18446744073709551616.0L ? 0ull : (unsigned long long)f;
         r->tab.axis[i] = (uint8_t)axis[i];
     }
+    try {
+        std::lock_guard<std::mutex> lk(g_mu);
+        g_ropes.insert(r);
+    } catch (...) {
+        delete r;
+        return ATTN_E_NOMEM;
+    }
     *out = r;
     return ATTN_OK;
 }
 
-ATTN_EXPORT void attn_rope_destroy(attn_rope_t rope) { delete rope; }
+ATTN_EXPORT void attn_rope_destroy(attn_rope_t rope) {
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!g_ropes.erase(rope)) return;
+    }
+    delete rope;
+}
 
 ATTN_EXPORT int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int64_t x_token_stride, int64_t T, int H,
                                 const int32_t *pos, int64_t pos_stride, int grad, void *out, int64_t out_token_stride,
                                 void *stream) {
     if (!rope || !x || !pos || !out) return ATTN_E_NULL;
+    if (!known(rope)) return ATTN_E_BAD_PLAN;
     const int size = dtype == ATTN_DTYPE_F32 ? 4 : 2;
     if (dtype != ATTN_DTYPE_BF16 && dtype != ATTN_DTYPE_F16 && dtype != ATTN_DTYPE_F32) return ATTN_E_UNSUPPORTED;
     if (T < 0 || T >= (1ll << 31) || H < 1 || H > 65536) return ATTN_E_INVALID_ARG;
@@ -349,6 +376,7 @@ ATTN_EXPORT int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void
                                   const int32_t *cu_k, void *stream) {
     if (!plan || !live(plan)) return ATTN_E_BAD_PLAN;
     if (!k || !v || !k_cache || !v_cache || !cu_q || !cu_k || (rope && !pos) || !q != !q_out) return ATTN_E_NULL;
+    if (rope && !known(rope)) return ATTN_E_BAD_PLAN;
     int rc = check_paging(plan, page_stride, token_stride, page_size, num_pages, block_table, bt_stride);
     if (rc != ATTN_OK) return rc;
     const attn_plan_desc &d = plan->d;
