@@ -1,4 +1,5 @@
-"""ctypes binding of libvgqa (include/varlen_gqa.h): argument marshalling only.
+"""Binding of libvgqa (include/varlen_gqa.h): argument marshalling only, by
+ctypes and, for the cache operators, by the native module _lib/_marshal.so.
 
 Every step of the attention runs in the library's CUDA kernels; this module
 checks dtypes, shapes and devices of torch tensors, passes their device
@@ -9,6 +10,8 @@ present, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -16,6 +19,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libvgqa.so")
+MARSHAL_PATH = os.path.join(_HERE, "_lib", "_marshal.so")
 
 ATTN_OK = 0
 ATTN_VARIANT_AUTO, ATTN_VARIANT_SIMT, ATTN_VARIANT_MMA, ATTN_VARIANT_TC = 0, 1, 2, 3
@@ -56,11 +60,12 @@ class AttnError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_marshal = None          # native marshalling of the cache operators, loaded with the library
 
 
 def lib() -> ctypes.CDLL:
     """Load libvgqa.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _marshal
     if _lib is not None:
         return _lib
     with _lock:
@@ -69,6 +74,8 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libvgqa.so not built ({LIB_PATH}); run "
                                "`python -m varlen_gqa_split_b200.build`")
+        if not os.path.exists(MARSHAL_PATH):
+            raise RuntimeError(f"_marshal.so not built ({MARSHAL_PATH}); run `python -m varlen_gqa_split_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         vp, i, i32p = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p
         L.attn_plan.argtypes = [ctypes.POINTER(vp), i, i, i, i, i, i]
@@ -111,6 +118,11 @@ def lib() -> ctypes.CDLL:
         L.attn_key_weights_paged.restype = i
         L.attn_evict_paged.argtypes = [vp, vp, i32p, i32p, i32p, i, i, vp, i32p, i64, vp, vp] + cache + [i32p, i32p, vp]
         L.attn_evict_paged.restype = i
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", MARSHAL_PATH)
+        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        loader.exec_module(m)
+        m.bind(LIB_PATH)
+        _marshal = m
         _lib = L
         return L
 
@@ -167,20 +179,6 @@ def _stream_ptr(stream) -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
-_ROPE_DTYPES = {torch.bfloat16: ATTN_DTYPE_BF16, torch.float16: ATTN_DTYPE_F16, torch.float32: ATTN_DTYPE_F32}
-
-
-def _heads_strided(name, t, T, H, D, dev):
-    """Address and token stride of t [T, H, D] on device `dev` whose heads are
-    contiguous within a token."""
-    if t.get_device() != dev or t.shape != (T, H, D):
-        raise ValueError(f"{name} must be a tensor [{T}, {H}, {D}] of CUDA device {dev}")
-    s = t.stride()
-    if (D > 1 and s[2] != 1) or (H > 1 and s[1] != D):
-        raise ValueError(f"{name} must keep each token's heads contiguous (strides (s, D, 1), s >= H*D)")
-    return t.data_ptr(), s[0] if T > 1 else max(s[0], H * D)
-
-
 def rope_table(n_pairs, sections=None, *, base=10000.0, restart=False):
     """freqs, axes for Rope: pair i of n turns with base^(-i / n) radians per
     position.  sections: pairs per axis, in order (None: one axis for all);
@@ -228,17 +226,6 @@ class Rope:
     def handle(self):
         return self._h
 
-    def _pos(self, pos, T, dev):
-        """Address and axis stride of pos [n_axes, T] (or [T] for one axis)."""
-        n = self.n_axes
-        if n == 1 and pos.dim() == 1:
-            pos = pos[None]
-        if pos.dtype is torch.int32 and pos.get_device() == dev and pos.shape == (n, T):
-            s = pos.stride()
-            if T <= 1 or s[1] == 1:
-                return pos.data_ptr(), s[0] if n > 1 else max(s[0], T)
-        raise ValueError(f"pos must be int32 [{n}, {T}] on CUDA device {dev}, unit stride over tokens")
-
     def apply(self, x, pos, out=None, *, grad=False, stream=None):
         """out = rope.apply(x, pos[, out, grad, stream]): rotate x [T, H, D]
         (bf16, fp16 or fp32; heads contiguous within a token, token stride
@@ -247,24 +234,10 @@ class Rope:
         itself; it is allocated packed when not given."""
         if self._h is None:
             raise AttnError(-3, "attn_rope_apply")
-        dtype = _ROPE_DTYPES.get(x.dtype)
-        if dtype is None:
-            raise TypeError("x must be bf16, fp16 or fp32")
-        dev = _raw_device()
-        if x.dim() != 3:
-            raise ValueError("x must be [T, H, D]")
-        T, H, D = x.shape[0], x.shape[1], self.D
-        xp, xs = _heads_strided("x", x, T, H, D, dev)
         if out is None:
-            out = torch.empty(T, H, D, dtype=x.dtype, device=x.device)
-        if out.dtype is not x.dtype:
-            raise ValueError("out must have x's type and shape")
-        op, os_ = _heads_strided("out", out, T, H, D, dev)
-        pp, ps = self._pos(pos, T, dev)
-        if T == 0 or H == 0:
-            return out
-        rc = lib().attn_rope_apply(self._h, dtype, xp, xs, T, H, pp, ps, 1 if grad else 0, op, os_,
-                                   _stream_ptr(stream))
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        rc = _marshal.rope_apply(self._h.value, self.D, self.n_axes, _raw_device(), x, pos, out, grad,
+                                 _stream_ptr(stream))
         if rc:
             _check(rc, "attn_rope_apply")
         return out
@@ -307,7 +280,8 @@ class Plan:
         self._h = h
         self.device = torch.cuda.current_device()
         self.info = self._info()
-        self._sizes = (*(self.info[n] for n in ("B_max", "Hq", "Hkv", "D")), self.device, self.info["s_max"])
+        # what the native marshalling checks tensors against
+        self._args = (h.value, *(self.info[n] for n in ("B_max", "Hq", "Hkv", "D")), self.device, self.info["s_max"])
 
     def _info(self) -> dict:
         d = PlanDesc()
@@ -388,53 +362,6 @@ class Plan:
         _check(rc, "attn_run_paged")
         return out, lse
 
-    def _paging(self, k_cache, v_cache, block_table):
-        """Addresses of the caches (v_cache None: keys only) and the cache
-        arguments of the paged entry points, in the C ABI's order."""
-        B, _, Hkv, D, dev, s_max = self._sizes
-        shape, s = k_cache.shape, k_cache.stride()
-        if k_cache.dtype is not torch.bfloat16 or k_cache.get_device() != dev:
-            raise TypeError("k_cache must be a bf16 tensor of the plan's device")
-        if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
-            raise ValueError(f"k_cache must be [num_pages, page_size, {Hkv}, {D}]")
-        if s[3] != 1 or (Hkv > 1 and s[2] != D):
-            raise ValueError("k_cache must keep each token's heads contiguous")
-        vp = None
-        if v_cache is not None:
-            if v_cache.dtype is not torch.bfloat16 or v_cache.get_device() != dev:
-                raise TypeError("v_cache must be a bf16 tensor of the plan's device")
-            if v_cache.shape != shape or v_cache.stride() != s:
-                raise ValueError("k_cache and v_cache must have the same shape and strides")
-            vp = v_cache.data_ptr()
-        n_pages, page_size = shape[0], shape[1]
-        tok = s[1] if page_size > 1 else Hkv * D
-        bt, bs = block_table.shape, block_table.stride()
-        if block_table.dtype is not torch.int32 or block_table.get_device() != dev or len(bt) != 2 or bt[0] != B or \
-                (bt[1] > 1 and bs[1] != 1):
-            raise ValueError("block_table must be an int32 tensor [B_max, n] of the plan's device, unit column stride")
-        if bt[1] * page_size < s_max:
-            raise ValueError("block_table rows must cover s_max keys")
-        return k_cache.data_ptr(), vp, (s[0] if n_pages > 1 else page_size * tok, tok, page_size, n_pages,
-                                        block_table.data_ptr(), bs[0] if B > 1 else max(bs[0], bt[1]))
-
-    def _per_sequence(self, name, t, n):
-        if t.dtype is torch.int32 and t.get_device() == self.device and t.numel() == n and t.is_contiguous():
-            return t.data_ptr()
-        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} entries on the plan's device")
-
-    def _ledger(self, name, t, dtype, shape):
-        """Address of a ledger array of `shape` [B_max, Hkv, ld >= s_max]."""
-        if t.dtype is dtype and t.get_device() == self.device and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} of the plan's device")
-
-    def _ledger_shape(self, name, t):
-        shape = t.shape
-        B, _, Hkv, _, _, s_max = self._sizes
-        if len(shape) != 3 or shape[0] != B or shape[1] != Hkv or shape[2] < s_max:
-            raise ValueError(f"{name} must be [{B}, {Hkv}, >= {s_max}]")
-        return shape
-
     def append_paged(self, k, v, k_cache, v_cache, block_table, cu_q, cu_k, *, q=None, pos=None, rope=None,
                      q_out=None, stream=None):
         """q_out = plan.append_paged(k, v, k_cache, v_cache, block_table, cu_q, cu_k, *[, q, pos, rope, q_out, stream]).
@@ -447,65 +374,41 @@ class Plan:
         through attn_append_paged."""
         if self._h is None:
             raise AttnError(-5, "attn_append_paged")
-        B, Hq, Hkv, D, dev, _ = self._sizes
-        T = k.shape[0]
-        if k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
-            raise TypeError("k and v must be bf16 tensors")
-        kp, ks = _heads_strided("k", k, T, Hkv, D, dev)
-        vp, vs = _heads_strided("v", v, T, Hkv, D, dev)
-        qp = op = rp = pp = None
-        qs = ps = 0
-        if q is not None:
-            if q.dtype is not torch.bfloat16:
-                raise TypeError("q must be a bf16 tensor")
-            qp, qs = _heads_strided("q", q, T, Hq, D, dev)
-            if q_out is None:
-                q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-            if q_out.dtype is not torch.bfloat16 or q_out.shape != (T, Hq, D) or not q_out.is_contiguous() or \
-                    q_out.get_device() != dev:
-                raise ValueError("q_out must be a contiguous bf16 tensor shaped like q, on its device")
-            op = q_out.data_ptr()
-        elif q_out is not None:
-            raise ValueError("q_out without q")
+        if q is None:
+            if q_out is not None:
+                raise ValueError("q_out without q")
+        elif q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        rp = n_axes = 0
         if rope is not None:
-            rp = rope._h
-            if rp is None:
+            if rope._h is None:
                 raise AttnError(-3, "attn_append_paged")
             if pos is None:
                 raise ValueError("rope needs pos")
-            pp, ps = rope._pos(pos, T, dev)
+            if rope.D != self.info["D"]:
+                raise ValueError("rope's head size is not the plan's")
+            rp, n_axes = rope._h.value, rope.n_axes
         elif pos is not None:
             raise ValueError("pos without rope")
-        cq, ck = self._per_sequence("cu_q", cu_q, B + 1), self._per_sequence("cu_k", cu_k, B + 1)
-        kc, vc, cache = self._paging(k_cache, v_cache, block_table)
-        if T:
-            rc = lib().attn_append_paged(self._h, rp, qp, qs, kp, ks, vp, vs, T, pp, ps, op, kc, vc, *cache, cq, ck,
-                                         _stream_ptr(stream))
-            if rc:
-                _check(rc, "attn_append_paged")
+        rc = _marshal.append_paged(self._args, rp, n_axes, k, v, k_cache, v_cache, block_table, cu_q, cu_k, q, pos, q_out,
+                                   _stream_ptr(stream))
+        if rc:
+            _check(rc, "attn_append_paged")
         return q_out
 
-    def _weights_args(self, q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream):
-        B, Hq, Hkv, D, dev, s_max = self._sizes
-        T = q.shape[0]
-        if q.dtype is not torch.bfloat16 or q.get_device() != dev or q.shape != (T, Hq, D) or not q.is_contiguous():
-            raise ValueError(f"q must be a contiguous bf16 tensor [T_q, {Hq}, {D}] of the plan's device")
-        if lse.dtype is not torch.float32 or lse.get_device() != dev or lse.shape != (T, Hq) or \
-                not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous fp32 tensor [T_q, Hq] of the plan's device")
-        if (seen is None) != (born is None):
-            raise ValueError("seen and born go together")
-        first = out if out is not None else weight_in if weight_in is not None else born
-        shape = (B, Hkv, s_max) if first is None else self._ledger_shape("the ledger", first)
+    def _key_weights(self, where, q, k, block_table, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream):
+        if self._h is None:
+            raise AttnError(-5, where)
         if out is None:
-            out = torch.zeros(shape, dtype=torch.float32, device=q.device)
-        ledger = (self._per_sequence("cu_q", cu_q, B + 1), self._per_sequence("cu_k", cu_k, B + 1),
-                  lse.data_ptr(), decay,
-                  None if weight_in is None else self._ledger("weight_in", weight_in, torch.float32, shape),
-                  self._ledger("out", out, torch.float32, shape), shape[2],
-                  None if seen is None else self._per_sequence("seen", seen, B),
-                  None if born is None else self._ledger("born", born, torch.int32, shape), _stream_ptr(stream))
-        return out, ledger
+            like = weight_in if weight_in is not None else born
+            i = self.info
+            out = torch.zeros((i["B_max"], i["Hkv"], i["s_max"] if like is None else like.shape[-1]),
+                              dtype=torch.float32, device=q.device)
+        rc = _marshal.key_weights(self._args, q, k, block_table, cu_q, cu_k, lse, weight_in, decay, out, seen, born,
+                                  _stream_ptr(stream))
+        if rc:
+            _check(rc, where)
+        return out
 
     def key_weights(self, q, k, cu_q, cu_k, lse, weight_in=None, *, decay=1.0, out=None, seen=None, born=None,
                     stream=None):
@@ -517,30 +420,17 @@ class Plan:
         as in run(), lse its result.  With seen [B_max] and born [B_max, Hkv,
         ld] int32, the births of the present tokens are written.  Goes through
         attn_key_weights."""
-        if self._h is None:
-            raise AttnError(-5, "attn_key_weights")
-        _, _, Hkv, D, dev, _ = self._sizes
-        if k.dtype is not torch.bfloat16:
-            raise TypeError("k must be a bf16 tensor")
-        kp, ks = _heads_strided("k", k, k.shape[0], Hkv, D, dev)
-        out, ledger = self._weights_args(q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream)
-        rc = lib().attn_key_weights(self._h, q.data_ptr(), kp, ks, *ledger)
-        if rc:
-            _check(rc, "attn_key_weights")
-        return out
+        return self._key_weights("attn_key_weights", q, k, None, cu_q, cu_k, lse, weight_in, decay, out, seen, born,
+                                 stream)
 
     def key_weights_paged(self, q, k_cache, block_table, cu_q, cu_k, lse, weight_in=None, *, decay=1.0, out=None,
                           seen=None, born=None, stream=None):
         """key_weights over a paged cache (k_cache and block_table as in
         run_paged).  Goes through attn_key_weights_paged."""
-        if self._h is None:
-            raise AttnError(-5, "attn_key_weights_paged")
-        kc, _, cache = self._paging(k_cache, None, block_table)
-        out, ledger = self._weights_args(q, cu_q, cu_k, lse, weight_in, decay, out, seen, born, stream)
-        rc = lib().attn_key_weights_paged(self._h, q.data_ptr(), kc, *cache, *ledger)
-        if rc:
-            _check(rc, "attn_key_weights_paged")
-        return out
+        if block_table is None:
+            raise ValueError("block_table must be a tensor")
+        return self._key_weights("attn_key_weights_paged", q, k_cache, block_table, cu_q, cu_k, lse, weight_in, decay,
+                                 out, seen, born, stream)
 
     def evict_paged(self, weight, born, seen, keep, k_cache, v_cache, block_table, cu_k, *, sink=0, recent=0,
                     weight_out=None, born_out=None, cu_k_out=None, stream=None):
@@ -556,25 +446,14 @@ class Plan:
         attn_evict_paged."""
         if self._h is None:
             raise AttnError(-5, "attn_evict_paged")
-        B = self._sizes[0]
-        shape = self._ledger_shape("weight", weight)
-        wp, bp = self._ledger("weight", weight, torch.float32, shape), self._ledger("born", born, torch.int32, shape)
-        wo, bo = wp, bp
         if weight_out is None:
             weight_out = weight
-        else:
-            wo = self._ledger("weight_out", weight_out, torch.float32, shape)
         if born_out is None:
             born_out = born
-        else:
-            bo = self._ledger("born_out", born_out, torch.int32, shape)
         if cu_k_out is None:
             cu_k_out = torch.empty_like(cu_k)
-        kc, vc, cache = self._paging(k_cache, v_cache, block_table)
-        rc = lib().attn_evict_paged(self._h, wp, bp, self._per_sequence("seen", seen, B),
-                                    self._per_sequence("keep", keep, B), sink, recent, wo, bo, shape[2], kc, vc, *cache,
-                                    self._per_sequence("cu_k", cu_k, B + 1),
-                                    self._per_sequence("cu_k_out", cu_k_out, B + 1), _stream_ptr(stream))
+        rc = _marshal.evict_paged(self._args, weight, born, seen, keep, k_cache, v_cache, block_table, cu_k, sink, recent,
+                                  weight_out, born_out, cu_k_out, _stream_ptr(stream))
         if rc:
             _check(rc, "attn_evict_paged")
         return weight_out, born_out, cu_k_out

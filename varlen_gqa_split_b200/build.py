@@ -24,6 +24,10 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "libvgqa.so")
+# the binding's native marshalling (a Python extension module; needs torch's
+# headers, calls the library through its C ABI)
+MARSHAL_SRC = os.path.join(CSRC, "python", "marshal.cpp")
+MARSHAL = os.path.join(LIBDIR, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-I", INCLUDE,
@@ -53,6 +57,29 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def marshal_up_to_date() -> bool:
+    deps = [MARSHAL_SRC, os.path.join(INCLUDE, "varlen_gqa.h"), os.path.abspath(__file__)]
+    return os.path.exists(MARSHAL) and all(os.path.getmtime(f) <= os.path.getmtime(MARSHAL) for f in deps)
+
+
+def build_marshal() -> str:
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include")]
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{d}" for d in inc] + \
+        [MARSHAL_SRC, "-o", tmp, "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def _compile(src: str, verbose: bool) -> tuple[str, str]:
     obj = os.path.join(OBJDIR, os.path.basename(src) + ".o")
     cmd = [nvcc()] + NVCC_FLAGS + ["-c", src, "-o", obj]
@@ -63,13 +90,19 @@ def _compile(src: str, verbose: bool) -> tuple[str, str]:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libvgqa.so; returns its path."""
+    """Compile and link libvgqa.so and the binding's marshalling module;
+    returns the library's path."""
+    os.makedirs(LIBDIR, exist_ok=True)
     if not force and up_to_date():
+        if not marshal_up_to_date():
+            build_marshal()
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
-    os.makedirs(LIBDIR, exist_ok=True)
     with concurrent.futures.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
+        module = ex.submit(build_marshal) if force or not marshal_up_to_date() else None
         results = list(ex.map(lambda s: _compile(s, verbose), sources()))
+        if module:
+            module.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
