@@ -39,9 +39,9 @@ namespace vgqa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 3;           // 80 registers a thread: with 4 some would spill (ragged prompts 89.6 us, 80.5 with 3)
 constexpr int kWarps = kThreads / 32;
-constexpr int kCopies = 4;                // histogram copies
+constexpr int kCopies = 2;                // histogram copies (64 units of 1044 keys x 8: 17.4 us, 4 take 17.8, 8 take 18.9)
 constexpr int kBatch = 8;                 // loads of a thread in flight
 constexpr int kMaxCluster = 8;
 constexpr int kCoarse = 4;                // words (of 32 keys) per entry of the prefix counts
@@ -462,7 +462,7 @@ namespace {
 
 cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
     // A cluster per unit: as many blocks as fill the device, but no slice
-    // under 1024 keys
+    // under 1024 keys (8 units of 32768 keys: 8 blocks each 20.0 us, 4 29.4)
     const long long units = (long long)p.B_max * p.Hkv;
     int cs = 1;
     while (cs < kMaxCluster && units * cs * 2 <= 148 * kBlocksPerSm && p.s_max >= 2048 * cs) cs *= 2;
@@ -470,7 +470,7 @@ cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
     const size_t fixed = sizeof(Head) + bits_bytes(p.s_max, cs), ranks = (size_t)e.slice_words * 32 * 4;
     e.cached = fixed + ranks <= (size_t)kMaxSmem ? e.slice_words * 32 : 0;
     return launch_dependent(evict_kernel, dim3((unsigned)((p.B_max * p.Hkv + 1) * cs)), dim3(kThreads),
-                            fixed + (e.cached ? ranks : 0), stream, cs, p, e);
+                            fixed + (e.cached ? ranks : 0), stream, cs > 1 ? cs : 0, p, e);
 }
 
 bool overlap(const void *a, const void *b, size_t na, size_t nb) {
