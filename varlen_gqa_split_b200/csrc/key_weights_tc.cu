@@ -68,6 +68,12 @@ struct SeqInfo {
     long long tot;            // positions of one KV head
 };
 
+// quotients of numbers that are nearly always small (a 64-bit division takes
+// some hundred cycles, in every block and role before its first load)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // row tiles that see key tile kt
 __device__ __forceinline__ int row_tiles(const SeqInfo &s, int kt, int qtile) {
     return min(s.nrt, (s.Lk - 1 - kt * kItemKeys) / qtile + 1);
@@ -105,31 +111,40 @@ __device__ __forceinline__ int block_of(long long pos, const Share &sh) { return
 __device__ bool block_share(const Params &p, int tid, long long *scan, long long *found, Share &sh) {
     const int per = (p.B_max + kThreads - 1) / kThreads;
     const int b0 = min(p.B_max, tid * per), b1 = min(p.B_max, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_info(p, b, blockIdx.x == 0).tot * p.Hkv;
+    long long mine = 0, one = 0;          // positions of the run, and of its last sequence
+    for (int b = b0; b < b1; ++b) {
+        one = seq_info(p, b, blockIdx.x == 0).tot * p.Hkv;
+        mine += one;
+    }
     long long inc = mine;
     const int lane = tid & 31, warp = tid >> 5;
-#pragma unroll
+#pragma unroll 1
     for (int d = 1; d < 32; d <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, inc, d);
         if (lane >= d) inc += o;
     }
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    long long T = 0;
-    for (int i = 0; i < kThreads / 32; ++i) {
-        if (i < warp) inc += scan[i];
-        T += scan[i];
+    // (short code: what runs once is paid for in instruction fetches)
+    long long T = lane < kThreads / 32 ? scan[lane] : 0, below = lane < warp ? T : 0;
+#pragma unroll 1
+    for (int d = 16; d; d >>= 1) {
+        T += __shfl_xor_sync(0xffffffffu, T, d);
+        below += __shfl_xor_sync(0xffffffffu, below, d);
     }
+    inc += below;
     sh.T = T;
     sh.C = (int)min((long long)gridDim.x, T);
     if ((int)blockIdx.x >= sh.C) return false;
-    sh.lo = T * blockIdx.x / sh.C;
-    sh.hi = T * (blockIdx.x + 1) / sh.C;
+    // T c / C, rounded down, for c and c + 1
+    const long long q = quotient(T, sh.C);
+    const uint32_t r = (uint32_t)(T - q * sh.C), c = blockIdx.x;
+    sh.lo = q * c + r * c / (uint32_t)sh.C;
+    sh.hi = q * (c + 1) + r * (c + 1) / (uint32_t)sh.C;
     long long at = inc - mine;
     if (sh.lo >= at && sh.lo < inc) {
         for (int b = b0; b < b1; ++b) {
-            const long long n = seq_info(p, b, false).tot * p.Hkv;
+            const long long n = per == 1 ? one : seq_info(p, b, false).tot * p.Hkv;
             if (sh.lo < at + n) {
                 found[0] = at;
                 found[1] = b;
@@ -163,12 +178,12 @@ struct Walker {
         hi = sh.hi;
         s = seq_info(p, b, false);
         long long rem = g - sh.pb;
-        hk = (int)(rem / s.tot);
+        hk = (int)quotient(rem, s.tot);
         rem -= hk * s.tot;
         P = g - rem;
         const int full = max(s.nrt, 1);
         if (rem < (long long)s.ksat * full) {
-            kt = (int)(rem / full);
+            kt = (int)quotient(rem, full);
             P += (long long)kt * full;
         } else {
             kt = s.ksat;
@@ -209,7 +224,9 @@ struct Walker {
 
 // sum over 16 columns of 2^(s scale + nl); MASKED: only those in `vis`.  Taking
 // some of the exponentials on the FMA pipe (a polynomial) was measured and
-// lost: 1 of 8 pairs 1.72 ms where none takes 1.73, 3 of 8 1.90.
+// lost, since four warps a scheduler wait on each other's latencies before
+// they exhaust the special-function unit: 1 of 16 columns 1.68 ms where none
+// takes 1.67, 3 of 16 1.79.
 template <bool MASKED>
 __device__ __forceinline__ void add_columns(const uint32_t (&v)[16], const float *nl, float2 scale, uint32_t vis,
                                             float2 (&acc)[2]) {
