@@ -536,7 +536,7 @@ int attn_key_weights_paged(attn_plan_t plan, const void *q, const void *k_cache,
  * the inputs a repeated call does the same again.  Rows and ledger entries at
  * c and above are left as they were; the pages past ceil(c / page_size) are
  * free.  A table entry outside the cache sets ATTN_DEV_ERR_PAGE and the moves
- * from or to it are left out.  Plans with s_max > 2^20 get ATTN_E_UNSUPPORTED.
+ * from or to it are left out.  Plans with s_max > 2^19 get ATTN_E_UNSUPPORTED.
  */
 int attn_evict_paged(attn_plan_t plan, const float *weight, const int32_t *born, const int32_t *seen,
                      const int32_t *keep, int sink, int recent, float *weight_out, int32_t *born_out, int64_t ld,

@@ -595,6 +595,36 @@ def test_evict_long(Hkv, lk, keep, weights):
     _check_evict(lk, keep, Hkv=Hkv, page=32, sink=4, recent=100, weights=weights)
 
 
+def test_evict_longest_plans():
+    """The largest length that eviction takes, with ties across all blocks of a
+    cluster and within one, of real lengths long and short."""
+    _check_evict([1 << 19], [1000], Hkv=1, page=64, weights="coarse")
+    _check_evict([(1 << 19) - 33, 70], [(1 << 19) - 40, 9], Hkv=1, page=64, weights="equal", s_max=1 << 19)
+
+
+def test_evict_zero_ties():
+    """The threshold among keys that were never looked at: they tie at zero."""
+    rng = np.random.default_rng(3)
+    for n, c, hkv in ((1044, 1020, 2), (9000, 8900, 2), (20000, 17000, 1)):
+        B, page, s_max = 2, 32, n
+        k = _bf16((2 * n, hkv, 64), n)
+        pc = W.paginate(k, k, np.array([0, n, 2 * n]), B, page, s_max, seed=n)
+        w = -np.log(rng.random((B, hkv, n))) ** 3
+        w[rng.random(w.shape) < 0.2] = 0.0
+        w[0, 0, ::7] = -0.0
+        w = w.astype(np.float32)
+        born = np.broadcast_to(np.arange(n, dtype=np.int32), w.shape).copy()
+        plan = Plan(B, s_max, hkv, hkv, 64, 1)
+        wo = torch.zeros(w.shape, device="cuda")
+        bo = torch.zeros(w.shape, dtype=torch.int32, device="cuda")
+        full = torch.full((B,), n, dtype=torch.int32, device="cuda")
+        plan.evict_paged(torch.from_numpy(w).cuda(), torch.from_numpy(born).cuda(), full, full * 0 + c, pc.k_cache,
+                         pc.v_cache, pc.block_table, _cu([n, n]), weight_out=wo, born_out=bo)
+        ref = _evict_host(w, born, [n, n], [n, n], [c, c], 0, 0)
+        for (b, h), (src, _) in ref.items():
+            assert np.array_equal(bo[b, h, :c].cpu().numpy(), born[b, h, src]), (n, b, h)
+
+
 def test_evict_many_long_units():
     """Enough units to fill the device with one block each, of more keys than
     a block keeps in shared memory."""
@@ -693,8 +723,8 @@ def test_refusals_with_a_plan():
     assert evict(kc=P(5) + 8) == -4 and evict(keep=P(12) + 1) == -4
     for c in bad_caches:
         assert evict(cache=c) == -1, c
-    big = Plan(1, (1 << 20) + 1, 1, 1, 64, 1)
-    assert L.attn_evict_paged(big.handle, P(0), P(1), P(13), P(12), 0, 0, P(2), P(3), (1 << 20) + 1, P(5), P(6), 2048, 64,
+    big = Plan(1, (1 << 19) + 1, 1, 1, 64, 1)
+    assert L.attn_evict_paged(big.handle, P(0), P(1), P(13), P(12), 0, 0, P(2), P(3), (1 << 19) + 1, P(5), P(6), 2048, 64,
                               16, 4, P(15), 1 << 20, P(14), P(11), None) == -2
     # the binding
     q, k = _bf16((4, 8, 64), 1), _bf16((20, 2, 64), 2)

@@ -17,7 +17,9 @@
 //   2. the c-th largest by radix selection, 8 bits at a time: a histogram of
 //      the digit over the keys that match the prefix so far, in copies to
 //      spread the collisions of alike weights, summed over the cluster's
-//      blocks through distributed shared memory.  It ends early once all keys of the digit stay;
+//      blocks through distributed shared memory.  It ends early once all keys
+//      of the digit stay, or all of them are alike (keys that were never
+//      looked at tie at zero);
 //   3. one bit per key, kept or not, and the counts of evicted places below c
 //      and of kept keys above, prefix-summed;
 //   4. the moves: pair i finds its place and its key by binary search in
@@ -113,6 +115,21 @@ __device__ void write_offsets(const Params &p, const Evict &e, int *scratch) {
     if (threadIdx.x == 0) e.cu_out[0] = 0;
 }
 
+// the place of the i-th set bit (from 0) of w, by halves
+__device__ __forceinline__ int nth_bit(uint32_t w, int i) {
+    int at = 0;
+#pragma unroll
+    for (int h = 16; h; h >>= 1) {
+        const int n = __popc(w & ((1u << h) - 1u));
+        if (i >= n) {
+            i -= n;
+            at += h;
+            w >>= h;
+        }
+    }
+    return at;
+}
+
 // the place of the i-th set bit (from 0) of the kCoarse words from entry a on
 __device__ __forceinline__ int pick(const uint32_t *bits, int a, int i, int words) {
     uint32_t x[kCoarse];
@@ -131,17 +148,7 @@ __device__ __forceinline__ int pick(const uint32_t *bits, int a, int i, int word
             w = x[k + 1];
         }
     }
-    // halve the word: is the bit in the lower part?
-#pragma unroll
-    for (int h = 16; h; h >>= 1) {
-        const int n = __popc(w & ((1u << h) - 1u));
-        if (i >= n) {
-            i -= n;
-            at += h;
-            w >>= h;
-        }
-    }
-    return at;
+    return at + nth_bit(w, i);
 }
 
 // Shared memory: this, then either the slice's ranks (steps 1 and 2) or, from
@@ -151,6 +158,7 @@ struct Head {
     uint32_t count[4][256];               // each pass's digit counts of this block (read by the cluster)
     uint32_t total[256];                  // and of the cluster
     int found[3];                         // the digit, the keys above it, the keys of it
+    uint32_t alike[4][2];                 // and, or of the ranks that a pass counted in this block
     int scratch[kWarps];
 };
 
@@ -191,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     const int last = seen - e.recent;
     const bool cached = e.cached >= per * 32;
     for (int i = tid; i < 256 * kCopies; i += kThreads) sh.hist[0][i] = 0;
+    if (tid < 8) sh.alike[tid >> 1][tid & 1] = tid & 1 ? 0u : ~0u;
     // one pass over the ledger: ranks into shared memory, entries below c to
     // the result (those of evicted keys are written again by the moves)
     if (cached || copy_w || copy_born)
@@ -235,16 +244,27 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     // with rank >> shift above `prefix`, and `need` of the `ties` equal to it stay
     uint32_t prefix = 0;
     int need = c, ties = n, shift = 32;
+    const uint32_t *tie_count = nullptr;                // this block's count of the last digit chosen
     for (int pass = 0; pass < 4 && ties != need; ++pass) {
         shift -= 8;
+        uint32_t all = ~0u, any = 0u;
         uint32_t *hist = sh.hist[pass & 1];
         for (int j0 = lo + tid; j0 < hi; j0 += kBatch * kThreads) {
             uint32_t u[kBatch];
             read_ranks(j0, 0u, u);
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
-                if (j0 + i * kThreads < hi && (pass == 0 || (u[i] >> (shift + 8)) == prefix))
+                if (j0 + i * kThreads < hi && (pass == 0 || (u[i] >> (shift + 8)) == prefix)) {
                     atomicAdd(&hist[((u[i] >> shift) & 255u) * kCopies + (lane % kCopies)], 1u);
+                    all &= u[i];
+                    any |= u[i];
+                }
+        }
+        all = __reduce_and_sync(0xffffffffu, all);
+        any = __reduce_or_sync(0xffffffffu, any);
+        if (lane == 0) {
+            atomicAnd(&sh.alike[pass][0], all);
+            atomicOr(&sh.alike[pass][1], any);
         }
         __syncthreads();
         uint32_t mine = 0;
@@ -260,6 +280,25 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
                 if (r < CS) mine += *cluster.map_shared_rank(&sh.count[pass][tid], r);
         }
         sh.total[tid] = mine;
+        all = ~0u;
+        any = 0u;
+        if (CS > 1) {
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r)
+                if (r < CS) {
+                    const uint32_t *theirs = cluster.map_shared_rank(&sh.alike[pass][0], r);
+                    all &= theirs[0];
+                    any |= theirs[1];
+                }
+        } else {
+            all = sh.alike[pass][0];
+            any = sh.alike[pass][1];
+        }
+        if (all == any && pass > 0) {                   // the same in all threads
+            prefix = all;
+            shift = 0;
+            break;
+        }
         __syncthreads();
         if (warp == 0) {
             // lane l: digits 255 - 8 l down to 248 - 8 l
@@ -296,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
         prefix = (prefix << 8) | (uint32_t)sh.found[0];
         need -= sh.found[1];
         ties = sh.found[2];
+        tie_count = &sh.count[pass][prefix & 255u];
     }
 
     // ---- bits: kept if above the threshold, or one of its first `need` ties.
@@ -305,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     uint32_t *bits = body + (cached ? e.cached : 0);
     uint32_t *pre = bits + e.slice_words * CS;          // [slice_words CS / kCoarse + 2] prefix counts
     const bool all_ties = ties == need;
+    uint32_t *tie_bits = pre + (e.slice_words * CS / kCoarse + 2);   // [slice_words]
     for (int j0 = lo + tid; j0 - lane < hi; j0 += kBatch * kThreads) {
         uint32_t u[kBatch];
         read_ranks(j0, 0u, u);
@@ -312,42 +353,31 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
         for (int i = 0; i < kBatch; ++i) {
             const int j = j0 + i * kThreads, first = j - lane;          // the word's first key
             if (first < hi) {
-                const uint32_t r = shift < 32 ? u[i] >> shift : 0u;
-                const uint32_t kept = __ballot_sync(0xffffffffu, j < hi && (r > prefix || (all_ties && r == prefix)));
+                const uint32_t r = u[i] >> shift;
+                const uint32_t above = __ballot_sync(0xffffffffu, j < hi && r > prefix);
+                const uint32_t tie = __ballot_sync(0xffffffffu, j < hi && r == prefix);
                 const uint32_t below = c - first >= 32 ? 0xffffffffu : c > first ? (1u << (c - first)) - 1u : 0u;
-                if (lane == 0) bits[first / 32] = kept ^ below;
+                if (lane == 0) {
+                    bits[first / 32] = (all_ties ? above | tie : above) ^ below;
+                    if (!all_ties) tie_bits[first / 32 - w0] = tie;
+                }
             }
         }
     }
     if (!all_ties) {
-        // the first ties in order (shift is 0 here): each warp a run of words,
-        // after the ties of the runs and, from their last digit's counts, of
-        // the blocks before it
-        __syncthreads();
-        const int wpw = (w1 - w0 + kWarps - 1) / kWarps;
-        const int ww0 = min(w1, w0 + warp * wpw), ww1 = min(w1, ww0 + wpw);
-        auto rank_at = [&](int j) -> uint32_t {
-            if (cached) return body[j - lo];
-            const int a = __ldcg(born + j);
-            return order_of(__ldcg(w + j), a < e.sink || a >= last);
-        };
+        // the first `need` ties in order: those of the blocks before this one
+        // count first, then a thread settles a word
         int before = 0;
-        for (int wd = ww0; wd < ww1; ++wd) {
-            const int j = wd * 32 + lane;
-            before += __popc(__ballot_sync(0xffffffffu, j < hi && rank_at(j) == prefix));
-        }
-        if (lane == 0) sh.scratch[warp] = before;
+        for (int r = 0; r < rank; ++r) before += (int)*cluster.map_shared_rank(tie_count, r);
         __syncthreads();
-        before = 0;
-        for (int i = 0; i < warp; ++i) before += sh.scratch[i];
-        for (int r = 0; r < rank; ++r) before += (int)*cluster.map_shared_rank(&sh.count[3][prefix & 255u], r);
-        for (int wd = ww0; wd < ww1; ++wd) {
-            const int j = wd * 32 + lane;
-            const uint32_t tie = __ballot_sync(0xffffffffu, j < hi && rank_at(j) == prefix);
-            const uint32_t kept = __ballot_sync(
-                0xffffffffu, (tie >> lane & 1u) && before + __popc(tie & ((1u << lane) - 1u)) < need);
-            before += __popc(tie);
-            if (lane == 0) bits[wd] ^= kept;
+        for (int i0 = w0; i0 < w1; i0 += kThreads) {
+            const int wd = i0 + tid;
+            const uint32_t tie = wd < w1 ? tie_bits[wd - w0] : 0u;
+            const int k = __popc(tie);
+            int total;
+            const int stay = need - before - (block_scan(k, sh.scratch, total) - k);     // of this word's ties
+            if (wd < w1 && stay > 0) bits[wd] ^= stay >= k ? tie : tie & ((1u << nth_bit(tie, stay)) - 1u);
+            before += total;
         }
     }
     // ---- every block gets the whole unit's bits
@@ -443,13 +473,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
 }
 
 constexpr int kMaxSmem = 200 * 1024;
-constexpr int kMaxKeys = 1 << 20;         // bits and counts of 2^20 keys take 160 KB
+constexpr int kMaxKeys = 1 << 19;         // bits, counts and ties of 2^19 keys take 144 KB
 
-// words of a slice, and shared memory, for clusters of `cs` blocks
+// words of a slice, and shared memory of the bits, for clusters of `cs` blocks
 int slice_words(int s_max, int cs) { return ((s_max + 31) / 32 + cs - 1) / cs; }
 size_t bits_bytes(int s_max, int cs) {
     const size_t words = (size_t)slice_words(s_max, cs) * cs;
-    return words * 4 + (words / kCoarse + 2) * 4;
+    return words * 4 + (words / kCoarse + 2) * 4 + (size_t)slice_words(s_max, cs) * 4;
 }
 
 }  // namespace
