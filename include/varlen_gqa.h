@@ -455,7 +455,7 @@ int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int64_t x_token_
  *   T_q      rows of q, k, v and pos, >= cu_q[B_max]
  *   q_out    device, bf16 [T_q, Hq, D] packed, 16-byte aligned: the rotated
  *            queries, ready for attn_run_paged.  q itself where q is packed,
- *            or apart from it
+ *            or apart from q, k and v
  *   pos      as in attn_rope_apply, for the T_q tokens
  *   k_cache .. bt_stride  as in attn_run_paged
  *   cu_q, cu_k  as in attn_run_paged: cu_k's lengths COUNT the new tokens, and
@@ -525,7 +525,7 @@ int attn_key_weights_paged(attn_plan_t plan, const void *q, const void *k_cache,
  *   k_cache .. bt_stride  as in attn_run_paged; rows move within the cache, so
  *            a sequence must not share its pages
  *   cu_k     device, int32 [B_max + 1]: the lengths before
- *   cu_k_out device, int32 [B_max + 1], apart from cu_k: 0 and the prefix sums
+ *   cu_k_out device, int32 [B_max + 1], apart from the inputs: 0 and the prefix sums
  *            of the lengths after (a sequence that breaks the plan's bounds
  *            sets its sticky bit, is left as it is, and counts as 0 here)
  *

@@ -687,6 +687,7 @@ def test_refusals_with_a_plan():
     assert append(qs=504) == -1 and append(ks=120) == -1 and append(vs=132) == -1
     assert append(q=P(0) + 8) == -4 and append(kc=P(5) + 8) == -4 and append(cq=P(14) + 2) == -4
     assert append(qo=P(0) + 1024) == -1 and append(qo=P(0), qs=640) == -1
+    assert append(qo=P(1)) == -1 and append(qo=P(2) + 16) == -1
     bad_caches = [(2040, 128, 16, 4, P(15), 4), (2048, 120, 16, 4, P(15), 4), (2048, 128, 12, 4, P(15), 4),
                   (2048, 128, 4, 4, P(15), 16), (2048, 128, 16, 0, P(15), 4), (2048, 128, 16, 4, P(15), 3)]
     for c in bad_caches:
@@ -719,7 +720,7 @@ def test_refusals_with_a_plan():
         assert evict(**{name: None}) == -3, name
     assert evict(sink=-1) == -1 and evict(recent=-1) == -1 and evict(ld=63) == -1
     assert evict(wo=P(0) + 4) == -1 and evict(bo=P(1) + 512) == -1 and evict(wo=P(1)) == -1 and evict(bo=P(2)) == -1
-    assert evict(co=P(14)) == -1 and evict(co=P(14) + 8) == -1 and evict(co=P(12)) == -1
+    assert evict(co=P(14)) == -1 and evict(co=P(14) + 8) == -1 and evict(co=P(12)) == -1 and evict(co=P(13)) == -1
     assert evict(kc=P(5) + 8) == -4 and evict(keep=P(12) + 1) == -4
     for c in bad_caches:
         assert evict(cache=c) == -1, c
@@ -842,6 +843,48 @@ def test_serving_loop():
             at += n_new
         assert s.lens.cpu().tolist() == [len(s.ref[b][0]["born"]) for b in range(B)]
         assert s.seen.cpu().tolist() == s.total
+
+
+def test_two_plans_on_two_streams():
+    """Two plans at work at once on streams of their own give what each gives
+    alone (nothing is shared between plans)."""
+    def make(seed, lq, lk, Hq, max_q):
+        Hkv, D = 2, 128
+        q, k = _bf16((int(np.sum(lq)), Hq, D), seed), _bf16((int(np.sum(lk)), Hkv, D), seed + 1)
+        pc = W.paginate(k, k, W.cu_from_lengths(lk), len(lk), 16, 4000, seed=seed)
+        x = dict(plan=Plan(len(lk), 4000, Hq, Hkv, D, max_q), q=q, pc=pc, cu_q=_cu(lq), cu_k=_cu(lk),
+                 lse=torch.full((q.shape[0], Hq), 9.0, device="cuda"), w=torch.zeros(len(lk), Hkv, 4000, device="cuda"),
+                 born=torch.zeros(len(lk), Hkv, 4000, dtype=torch.int32, device="cuda"),
+                 seen=torch.tensor(lk, dtype=torch.int32, device="cuda"), wo=torch.zeros(len(lk), Hkv, 4000, device="cuda"),
+                 bo=torch.zeros(len(lk), Hkv, 4000, dtype=torch.int32, device="cuda"),
+                 keep=torch.full((len(lk),), 500, dtype=torch.int32, device="cuda"),
+                 cu_new=torch.zeros(len(lk) + 1, dtype=torch.int32, device="cuda"))
+        return x
+
+    def run(x):
+        x["plan"].key_weights_paged(x["q"], x["pc"].k_cache, x["pc"].block_table, x["cu_q"], x["cu_k"], x["lse"],
+                                    out=x["w"], seen=x["seen"], born=x["born"])
+        x["plan"].evict_paged(x["w"], x["born"], x["seen"], x["keep"], x["pc"].k_cache, x["pc"].v_cache,
+                              x["pc"].block_table, x["cu_k"], recent=10, weight_out=x["wo"], born_out=x["bo"],
+                              cu_k_out=x["cu_new"])
+
+    args = [(1, [700, 30], [3900, 2000], 16, 700), (2, [1, 1, 1], [4000, 1200, 7], 8, 1)]
+    alone = []
+    for a in args:
+        x = make(*a)
+        run(x)
+        torch.cuda.synchronize()
+        alone.append((x["w"].clone(), x["bo"].clone(), x["pc"].k_cache.clone()))
+    both = [make(*a) for a in args]
+    streams = [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    for x, s in zip(both, streams):
+        with torch.cuda.stream(s):
+            run(x)
+    torch.cuda.synchronize()
+    for x, (w, bo, kc) in zip(both, alone):
+        assert x["plan"].check_error() == 0
+        assert torch.equal(x["w"], w) and torch.equal(x["bo"], bo) and torch.equal(_bits(x["pc"].k_cache), _bits(kc))
 
 
 def test_first_calls_inside_a_capture():

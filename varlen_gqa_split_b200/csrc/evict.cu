@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
                 const int i = q + u * pp + sub;
                 const long long from = __shfl_sync(0xffffffffu, from_at, i & 31);
                 const long long to = __shfl_sync(0xffffffffu, to_at, i & 31);
-                if (i < np && to >= 0) val[u] = *reinterpret_cast<const uint4 *>(cache + from);
+                if (i < np && to >= 0) val[u] = __ldcg(reinterpret_cast<const uint4 *>(cache + from));
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
@@ -540,7 +540,7 @@ ATTN_EXPORT int attn_evict_paged(attn_plan_t plan, const float *weight, const in
     if ((weight_out != weight && overlap(weight, weight_out, led, led)) ||
         (born_out != born && overlap(born, born_out, led, led)) || overlap(weight_out, born_out, led, led) ||
         overlap(weight_out, born, led, led) || overlap(born_out, weight, led, led) ||
-        overlap(cu_k, cu_k_out, cu, cu) || overlap(keep, cu_k_out, cu - 4, cu))
+        overlap(cu_k, cu_k_out, cu, cu) || overlap(keep, cu_k_out, cu - 4, cu) || overlap(seen, cu_k_out, cu - 4, cu))
         return ATTN_E_INVALID_ARG;
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_E_CUDA;

@@ -392,12 +392,14 @@ ATTN_EXPORT int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void
     for (const void *ptr : {q, k, v, (const void *)q_out, (const void *)k_cache, (const void *)v_cache})
         if (!aligned(ptr, 16)) return ATTN_E_ALIGNMENT;
     if (!aligned(cu_q, 4) || !aligned(cu_k, 4) || !aligned(pos, 4)) return ATTN_E_ALIGNMENT;
-    // q_out is q itself (packed) or apart from it
-    if (q && q_out != q && T_q > 0) {
-        const char *a = static_cast<const char *>(q), *b = static_cast<const char *>(q_out);
-        if (a < b + T_q * qrow * 2 && b < a + ((T_q - 1) * q_token_stride + qrow) * 2) return ATTN_E_INVALID_ARG;
-    } else if (q && q_token_stride != qrow) {
-        return ATTN_E_INVALID_ARG;
+    // q_out is q itself (packed) or apart from all that is read
+    if (q && T_q > 0) {
+        auto overlaps = [&](const void *in, long long stride, long long row) {
+            const char *a = static_cast<const char *>(in), *b = static_cast<const char *>(q_out);
+            return a < b + T_q * qrow * 2 && b < a + ((T_q - 1) * stride + row) * 2;
+        };
+        if (q_out == q ? q_token_stride != qrow : overlaps(q, q_token_stride, qrow)) return ATTN_E_INVALID_ARG;
+        if (q_out != q && (overlaps(k, k_token_stride, krow) || overlaps(v, v_token_stride, krow))) return ATTN_E_INVALID_ARG;
     }
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_E_CUDA;
