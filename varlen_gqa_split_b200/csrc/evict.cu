@@ -161,6 +161,7 @@ struct Head {
     uint32_t total[256];                  // and of the cluster
     int found[3];                         // the digit, the keys above it, the keys of it
     uint32_t alike[4][2];                 // and, or of the ranks that a pass counted in this block
+    uint32_t all, any;                    // and of the cluster
     int scratch[kWarps];
 };
 
@@ -272,36 +273,42 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
         uint32_t mine = 0;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) mine += hist[tid * kCopies + ((i + lane) % kCopies)];
-        sh.count[pass][tid] = mine;
         for (int i = tid; i < 256 * kCopies; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;
+        sh.count[pass][tid] = mine;
         if (CS > 1) {
+            // four digits a thread and, in another warp, a block's ranks a lane
             cluster.sync();
-            mine = 0;
+            if (tid < 64) {
+                uint4 sum = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                if (r < CS) mine += *cluster.map_shared_rank(&sh.count[pass][tid], r);
-        }
-        sh.total[tid] = mine;
-        all = ~0u;
-        any = 0u;
-        if (CS > 1) {
-#pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r)
-                if (r < CS) {
-                    const uint32_t *theirs = cluster.map_shared_rank(&sh.alike[pass][0], r);
-                    all &= theirs[0];
-                    any |= theirs[1];
+                for (int r = 0; r < kMaxCluster; ++r)
+                    if (r < CS) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(&sh.count[pass][4 * tid], r));
+                        sum = make_uint4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+                    }
+                *reinterpret_cast<uint4 *>(&sh.total[4 * tid]) = sum;
+            } else if (warp == 2) {
+                const uint32_t *theirs = cluster.map_shared_rank(&sh.alike[pass][0], min(lane, CS - 1));
+                all = __reduce_and_sync(0xffffffffu, theirs[0]);
+                any = __reduce_or_sync(0xffffffffu, theirs[1]);
+                if (lane == 0) {
+                    sh.all = all;
+                    sh.any = any;
                 }
+            }
         } else {
-            all = sh.alike[pass][0];
-            any = sh.alike[pass][1];
+            sh.total[tid] = mine;
+            if (tid == 0) {
+                sh.all = sh.alike[pass][0];
+                sh.any = sh.alike[pass][1];
+            }
         }
-        if (all == any && pass > 0) {                   // the same in all threads
-            prefix = all;
+        __syncthreads();
+        if (pass > 0 && sh.all == sh.any) {             // the same in all threads
+            prefix = sh.all;
             shift = 0;
             break;
         }
-        __syncthreads();
         if (warp == 0) {
             // lane l: digits 255 - 8 l down to 248 - 8 l
             uint32_t d[8];
@@ -385,11 +392,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     // ---- every block gets the whole unit's bits
     if (CS > 1) {
         cluster.sync();
-        for (int r = 0; r < CS; ++r) {
-            if (r == rank) continue;
-            const uint32_t *src = cluster.map_shared_rank(bits, r);
-            const int a0 = min(words, r * per), a1 = min(words, a0 + per);
-            for (int i = a0 + tid; i < a1; i += kThreads) bits[i] = src[i];
+        for (int i0 = tid; i0 < words; i0 += 4 * kThreads) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * kThreads;
+                x[k] = i < words ? cluster.map_shared_rank(bits, i / per)[i] : 0u;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + k * kThreads;
+                if (i < words && (i < w0 || i >= w1)) bits[i] = x[k];
+            }
         }
         cluster.sync();                                 // also: nobody leaves while others read its memory
     } else {
