@@ -61,11 +61,12 @@ def _rotate64(x, pos, freqs, axes, layout, scale=1.0, grad=False):
     return y, mag
 
 
-def _check_rotation(out, ref, mag):
+def _check_rotation(out, ref, mag, ref_angle=0.0):
     """One rounding to the type; before it the angle is off by at most pi 2^-25
     rad, cosine and sine (float, two units in the last place) by 2^-22, and
-    two products and a sum add 3 * 2^-24, all relative to |u| + |w|."""
-    tol = ref.abs() * EPS[out.dtype] + mag * (math.pi * 2.0 ** -25 + 2.0 ** -22 + 3 * 2.0 ** -24)
+    two products and a sum add 3 * 2^-24, all relative to |u| + |w|; so is what
+    the reference's own angle is off by (ref_angle, rad)."""
+    tol = ref.abs() * EPS[out.dtype] + mag * (math.pi * 2.0 ** -25 + 2.0 ** -22 + 3 * 2.0 ** -24 + ref_angle)
     tol = tol * (1 + 2.0 ** -7)             # the rounding is relative to the unrounded value
     if out.dtype == torch.float16:
         tol = tol + 2.0 ** -25              # half a step of fp16's subnormals
@@ -111,8 +112,9 @@ def test_rope_far_positions_and_scale():
     x = torch.randn(500, 2, 64, generator=_gen(1), device="cuda")
     pos = _positions(3, 500, 4)
     ref, mag = _rotate64(x, pos, freqs, axes, "half", 1.25)
-    # the reference's own product pos * f is rounded in 64 bits: 2^31 * 2^-53
-    _check_rotation(rope.apply(x, pos), ref, mag * (1 + 2.0 ** -21 / 2.0 ** -23 * 2.0 ** -2))
+    # the reference's own product pos * f (f <= 1) is rounded in 64 bits: 2^31 *
+    # 2^-53 rad at most; the table's turns are off by 2^31 * 2^-65 turns
+    _check_rotation(rope.apply(x, pos), ref, mag, 2.0 ** -22 + 2.0 ** -34 * 2 * math.pi)
 
 
 @pytest.mark.parametrize("off", [0, 8, 4, 1])
