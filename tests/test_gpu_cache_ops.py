@@ -237,6 +237,28 @@ def test_append_paged(page, fused, Hq, Hkv, D, n, layout):
     assert torch.equal(qp[:live], q_out[:live]) and torch.equal(qp[live:], q[live:])
 
 
+def test_append_reads_what_the_call_before_it_wrote():
+    """Rotation into a buffer and append from it, nothing between them in the
+    stream: every key of every repetition is that repetition's."""
+    B, L, Hkv, D, page = 4, 1024, 8, 128, 64
+    T = B * L
+    pc = _cache([L] * B, page, Hkv, D, L, 21)
+    plan = Plan(B, L, Hkv, Hkv, D, L)
+    rope, cu = Rope(D, *rope_table(64)), _cu([L] * B)
+    xs = [_bf16((T, Hkv, D), 30 + i) for i in range(4)]
+    pos = _positions(1, T, 22, 0, 1 << 16)
+    refs = [rope.apply(x, pos) for x in xs]
+    k = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    rows = pc.block_table[:, :L // page].long().flatten()
+    torch.cuda.synchronize()
+    for i in range(12):
+        rope.apply(xs[i % 4], pos, k)
+        plan.append_paged(k, k, pc.k_cache, pc.v_cache, pc.block_table, cu, cu)
+        for cache in (pc.k_cache, pc.v_cache):
+            assert torch.equal(_bits(cache[rows].reshape(T, Hkv, D)), _bits(refs[i % 4])), i
+    assert plan.check_error() == 0
+
+
 def test_append_errors_are_reported_and_contained():
     Hq, Hkv, D, page, s_max, B = 2, 1, 64, 16, 64, 4
     pc = _cache([64] * B, page, Hkv, D, s_max, 4)

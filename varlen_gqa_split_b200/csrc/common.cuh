@@ -392,15 +392,6 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t *p) {
     return v;
 }
 
-// Programmatic dependent launch: wait until the work before this kernel in the
-// stream is complete and visible, then let the next one be launched (its
-// blocks wait in turn).  Every kernel launched with the attribute starts with
-// this, before its first read of global memory.
-__device__ __forceinline__ void dependent_start() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // named barrier over `nthreads` threads (a subset of the block)
 __device__ __forceinline__ void named_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

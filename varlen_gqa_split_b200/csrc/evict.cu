@@ -172,7 +172,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int unit = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    dependent_start();
     if (unit == p.B_max * p.Hkv) {        // the extra cluster
         if (rank == 0) write_offsets(p, e, sh.scratch);
         return;
@@ -515,7 +514,7 @@ cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
     e.slice_words = slice_words(p.s_max, cs);
     const size_t fixed = sizeof(Head) + bits_bytes(p.s_max, cs), ranks = (size_t)e.slice_words * 32 * 4;
     e.cached = fixed + ranks <= (size_t)kMaxSmem ? e.slice_words * 32 : 0;
-    return launch_dependent(evict_kernel, dim3((unsigned)((p.B_max * p.Hkv + 1) * cs)), dim3(kThreads),
+    return launch_grid(evict_kernel, dim3((unsigned)((p.B_max * p.Hkv + 1) * cs)), dim3(kThreads),
                             fixed + (e.cached ? ranks : 0), stream, cs > 1 ? cs : 0, p, e);
 }
 

@@ -9,27 +9,26 @@ namespace vgqa {
 
 struct Params;
 
-// A launch as a programmatic dependent of the work before it in the stream
-// (the kernel starts with dependent_start); in clusters of `cluster` blocks
-// where it is not zero.  Takes about 0.6 us off a small call that follows
-// another (rope of 64 tokens 3.45 -> 2.88 us).
+// A plain launch, in clusters of `cluster` blocks where it is not zero: the
+// kernel starts when all work before it in the stream is complete and visible.
+// (Starting the cache operators as programmatic dependents took about 0.6 us
+// off a small call; they read lengths, tables and births that the kernel before
+// them may have written, and are kept to the plain order.)
 template <typename... A>
-cudaError_t launch_dependent(void (*fn)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
-                             const A &...args) {
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+cudaError_t launch_grid(void (*fn)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
+                        const A &...args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster ? 2 : 1;
+    cfg.numAttrs = cluster ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 

@@ -16,7 +16,7 @@ struct KeyWeights {
     float decay;
     float *part;               // tensor-core path: two parts of 256 sums per block, for items cut
                                // between blocks (NULL where one row tile holds all rows: no cuts)
-    uint32_t *ticket;          // and counts of finished parts, four per block
+    uint32_t *ticket;          // and counts of finished parts, eight per block (one a warp)
 };
 
 }  // namespace vgqa

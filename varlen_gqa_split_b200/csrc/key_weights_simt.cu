@@ -23,7 +23,6 @@ template <int D>
 __global__ void __launch_bounds__(kKeys) key_weights_simt_kernel(const Params p, const KeyWeights kw) {
     __shared__ float4 qs[kRowsStep][D / 4];
     __shared__ float nl[kRowsStep];       // -lse in base 2
-    dependent_start();
     const int b = blockIdx.z, hk = blockIdx.y, tid = threadIdx.x;
     int q0, Lq, k0, Lk;
     if (!load_lengths(p, b, blockIdx.x == 0 && hk == 0 && tid == 0, q0, Lq, k0, Lk)) return;
@@ -105,7 +104,7 @@ __global__ void __launch_bounds__(kKeys) key_weights_simt_kernel(const Params p,
 
 cudaError_t launch_key_weights_simt(const Params &p, const KeyWeights &kw, cudaStream_t stream) {
     const dim3 grid((p.s_max + kKeys - 1) / kKeys, p.Hkv, p.B_max);
-    return launch_dependent(p.D == 64 ? key_weights_simt_kernel<64> : key_weights_simt_kernel<128>, grid, dim3(kKeys), 0,
+    return launch_grid(p.D == 64 ? key_weights_simt_kernel<64> : key_weights_simt_kernel<128>, grid, dim3(kKeys), 0,
                             stream, 0, p, kw);
 }
 

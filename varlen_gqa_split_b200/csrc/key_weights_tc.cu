@@ -303,7 +303,6 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
         tc::tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
         tc::tmem_relinquish();
     }
-    dependent_start();
     Share sh;
     const bool has_work = block_share(p, tid, scan, found, sh);
     tc::fence_before_sync();
@@ -701,7 +700,7 @@ cudaError_t launch_key_weights_tc(const Params &p, const KeyWeights &kw, const C
     Kernel fn;
     size_t smem;
     pick(p.D, columns, p.block_table != nullptr, fn, smem);
-    return launch_dependent(fn, dim3(ctas), dim3(kThreads), smem, stream, 0, tm_q, tm_k, p, kw);
+    return launch_grid(fn, dim3(ctas), dim3(kThreads), smem, stream, 0, tm_q, tm_k, p, kw);
 }
 
 }  // namespace vgqa

@@ -77,7 +77,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 const int32_t *__restrict__ pos, long long ps, float sign, T *out, long long os, int groups, int lanes,
                 int tokens) {
     extern __shared__ float2 cs[];
-    dependent_start();
     const int n = tab.n;
     const long long t0 = (long long)blockIdx.x * tokens;
     const int nt = (int)min((long long)tokens, n_tok - t0);
@@ -242,7 +241,7 @@ cudaError_t launch_rope(const attn_rope_s &r, const void *x, long long xs, long 
     if (sh.blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     const size_t smem = (size_t)sh.tokens * r.tab.n * sizeof(float2);
     auto *fn = r.layout == ATTN_ROPE_HALF ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
-    return launch_dependent(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, r.tab,
+    return launch_grid(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, r.tab,
                             static_cast<const T *>(x), xs, n_tok, H, r.D, pos, ps, grad ? -1.f : 1.f,
                             static_cast<T *>(out), os, sh.groups, sh.lanes, sh.tokens);
 }
@@ -257,7 +256,7 @@ cudaError_t launch_append(const RopeTable &tab, bool half, const Params &p, Appe
     ap.tokens = sh.tokens;
     const size_t smem = (size_t)sh.tokens * (tab.n * sizeof(float2) + sizeof(long long) + sizeof(int2));
     auto *fn = half ? append_kernel<V, true> : append_kernel<V, false>;
-    return launch_dependent(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, tab, p, ap);
+    return launch_grid(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, tab, p, ap);
 }
 
 }  // namespace
