@@ -479,6 +479,8 @@ int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void *q, int64_t
  *
  *   q, k, cu_q, cu_k  as in attn_run_strided (the same tensors, after
  *            rotation); k_token_stride as there
+ *   T_q, T_kv  rows of q and lse, and of k: at least cu_q[B_max] and
+ *            cu_k[B_max].  No row of q or k past them is read
  *   lse      device, fp32 [T_q, Hq]: the call's attn_run* result
  *   weight_in, weight_out  device, fp32 ledgers of leading dimension ld; in may
  *            be NULL (nothing gathered yet), or out itself, or apart from it
@@ -498,14 +500,14 @@ int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void *q, int64_t
  * plan's bounds sets the plan's sticky bit and is left unwritten.  Sums run in
  * a fixed order: repeated calls give the same bits.
  */
-int attn_key_weights(attn_plan_t plan, const void *q, const void *k, int64_t k_token_stride, const int32_t *cu_q,
-                     const int32_t *cu_k, const float *lse, float decay, const float *weight_in, float *weight_out,
+int attn_key_weights(attn_plan_t plan, const void *q, int64_t T_q, const void *k, int64_t k_token_stride, int64_t T_kv,
+                     const int32_t *cu_q, const int32_t *cu_k, const float *lse, float decay, const float *weight_in, float *weight_out,
                      int64_t ld, const int32_t *seen, int32_t *born, void *stream);
 
 /* attn_key_weights over a paged cache (arguments of the cache as in
  * attn_run_paged; a table entry outside it sets ATTN_DEV_ERR_PAGE and its keys
  * count as zeros). */
-int attn_key_weights_paged(attn_plan_t plan, const void *q, const void *k_cache, int64_t page_stride,
+int attn_key_weights_paged(attn_plan_t plan, const void *q, int64_t T_q, const void *k_cache, int64_t page_stride,
                            int64_t token_stride, int page_size, int num_pages, const int32_t *block_table,
                            int bt_stride, const int32_t *cu_q, const int32_t *cu_k, const float *lse, float decay,
                            const float *weight_in, float *weight_out, int64_t ld, const int32_t *seen, int32_t *born,

@@ -86,8 +86,8 @@ def test_plan_entry_points_refuse_unknown_plans(L):
     cache = (1024, 256, 16, 4, p, 8)
     for plan in (None, 0x1234):
         assert L.attn_append_paged(plan, None, p, 256, p, 256, p, 256, 4, p, 4, p, p, p, *cache, p, p, None) == BAD_PLAN
-        assert L.attn_key_weights(plan, p, p, 256, p, p, p, 1.0, p, p, 64, None, None, None) == BAD_PLAN
-        assert L.attn_key_weights_paged(plan, p, p, *cache, p, p, p, 1.0, p, p, 64, None, None, None) == BAD_PLAN
+        assert L.attn_key_weights(plan, p, 4, p, 256, 8, p, p, p, 1.0, p, p, 64, None, None, None) == BAD_PLAN
+        assert L.attn_key_weights_paged(plan, p, 4, p, *cache, p, p, p, 1.0, p, p, 64, None, None, None) == BAD_PLAN
         assert L.attn_evict_paged(plan, p, p, p, p, 0, 0, p, p, 64, p, p, *cache, p, p, None) == BAD_PLAN
 
 

@@ -485,6 +485,30 @@ def test_key_weights_skips_rows_without_a_normaliser(Hq, Hkv, max_q, lq):
     assert ((out.double() - ref).abs() <= tol).all()
 
 
+@pytest.mark.parametrize("lk", [[20, 17, 18, 12], [1, 1], [127], [0, 5, 0], [60, 67, 1, 300]])
+def test_key_weights_short_packed_buffers(lk):
+    """Keys that end fewer than a tile's 128 rows behind the buffer's first
+    row: the last few rows of a larger buffer, NaN around them."""
+    B, Hq, Hkv, D, s_max = len(lk), 28, 4, 128, 320
+    T = sum(lk)
+    room = _bf16((T + 400, Hkv, D), 71)
+    room[:200] = float("nan")
+    room[200 + T:] = float("nan")
+    k, q = room[200:200 + T], _bf16((B, Hq, D), 72)
+    lq = np.ones(B, np.int64)
+    at = np.cumsum([0] + lk)
+    keys = [k[at[b]:at[b + 1]] for b in range(B)]
+    lse = _lse64(q, keys, lq, lk, Hq // Hkv)
+    ref, tol = _weights64(q, keys, lq, lk, lse, Hq // Hkv, 0.0, None, Hkv, s_max)
+    plan = Plan(B, s_max, Hq, Hkv, D, 1)
+    out = torch.full((B, Hkv, s_max), SENTINEL, device="cuda")
+    plan.key_weights(q, k, _cu(lq), _cu(lk), lse, out=out)
+    assert plan.check_error() == 0
+    for b in range(B):
+        assert ((out[b, :, :lk[b]].double() - ref[b, :, :lk[b]]).abs() <= tol[b, :, :lk[b]]).all(), b
+        assert (out[b, :, lk[b]:] == SENTINEL).all()
+
+
 def test_key_weights_errors_are_reported_and_contained():
     B, Hq, Hkv, D, s_max = 3, 8, 2, 64, 100
     q, k = _bf16((9, Hq, D), 1), _bf16((300, Hkv, D), 2)
@@ -720,11 +744,11 @@ def test_refusals_with_a_plan():
     assert append(cache=(2048, 128, 16, 4, P(15) + 1, 4)) == -4
 
     def weights(q=P(0), k=P(1), ks=128, cq=P(14), ck=P(14), lse=P(2), decay=1.0, wi=P(3), wo=P(4), ld=64, seen=P(13),
-                born=P(5), cache=None):
+                born=P(5), cache=None, T=4, Tk=20):
         tail = (cq, ck, lse, decay, wi, wo, ld, seen, born, None)
         if cache:
-            return L.attn_key_weights_paged(h, q, k, *cache, *tail)
-        return L.attn_key_weights(h, q, k, ks, *tail)
+            return L.attn_key_weights_paged(h, q, T, k, *cache, *tail)
+        return L.attn_key_weights(h, q, T, k, ks, Tk, *tail)
 
     for name in ("q", "k", "cq", "ck", "lse", "wo", "seen", "born"):
         assert weights(**{name: None}) == -3, name
@@ -732,6 +756,8 @@ def test_refusals_with_a_plan():
     assert weights(ks=120) == -1 and weights(ks=132) == -1 and weights(ld=63) == -1
     assert weights(decay=-1.0) == -1 and weights(decay=math.nan) == -1 and weights(decay=math.inf) == -1
     assert weights(wo=P(3) + 64) == -1 and weights(born=P(4)) == -1 and weights(born=P(3)) == -1
+    assert weights(T=-1) == -1 and weights(T=1 << 31) == -1 and weights(Tk=-1) == -1 and weights(Tk=1 << 31) == -1
+    assert weights(T=-1, cache=cache) == -1
     assert weights(q=P(0) + 8) == -4 and weights(lse=P(2) + 2) == -4
     for c in bad_caches:
         assert weights(cache=c) == -1, c

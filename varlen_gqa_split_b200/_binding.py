@@ -112,9 +112,9 @@ def lib() -> ctypes.CDLL:
                                         [i32p, i32p, vp])
         L.attn_append_paged.restype = i
         ledger = [i32p, i32p, vp, f32, vp, vp, i64, i32p, i32p, vp]
-        L.attn_key_weights.argtypes = [vp, vp, vp, i64] + ledger
+        L.attn_key_weights.argtypes = [vp, vp, i64, vp, i64, i64] + ledger
         L.attn_key_weights.restype = i
-        L.attn_key_weights_paged.argtypes = [vp, vp, vp] + cache + ledger
+        L.attn_key_weights_paged.argtypes = [vp, vp, i64, vp] + cache + ledger
         L.attn_key_weights_paged.restype = i
         L.attn_evict_paged.argtypes = [vp, vp, i32p, i32p, i32p, i, i, vp, i32p, i64, vp, vp] + cache + [i32p, i32p, vp]
         L.attn_evict_paged.restype = i

@@ -126,9 +126,9 @@ namespace vgqa {
 // [T, Hq, D] bf16, box = 64 elements x G heads x qtile tokens: one unit's
 // query rows (token-major, heads inner) as the tcgen05 kernel's A operand.
 // Loads are right-aligned to the sequence's last query token, so, as for K/V,
-// the token extent is left open.
-int encode_q_map(CUtensorMap *map, const void *base, int Hq, int D, int G, int qtile) {
-    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)0x7fffffff};
+// the token extent may be left open.
+int encode_q_map(CUtensorMap *map, const void *base, int Hq, int D, int G, int qtile, long long rows) {
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)Hq * D * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)qtile};
     cuuint32_t estr[3] = {1, 1, 1};

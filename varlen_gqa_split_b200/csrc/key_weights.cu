@@ -9,7 +9,7 @@ using namespace vgqa;
 
 namespace {
 
-int key_weights(attn_plan_t plan, const void *q, const void *k, long long k_stride, const Paging *pg,
+int key_weights(attn_plan_t plan, const void *q, long long T_q, const void *k, long long k_stride, long long T_kv, const Paging *pg,
                 const int32_t *cu_q, const int32_t *cu_k, const float *lse, float decay, const float *weight_in,
                 float *weight_out, int64_t ld, const int32_t *seen, int32_t *born, void *stream) {
     if (!q || !k || !cu_q || !cu_k || !lse || !weight_out || !seen != !born) return ATTN_E_NULL;
@@ -18,6 +18,7 @@ int key_weights(attn_plan_t plan, const void *q, const void *k, long long k_stri
                             (const void *)weight_out, (const void *)seen, (const void *)born})
         if (!aligned(ptr, 4)) return ATTN_E_ALIGNMENT;
     const attn_plan_desc &d = plan->d;
+    if (T_q < 0 || T_q >= (1ll << 31) || T_kv < 0 || T_kv >= (1ll << 31)) return ATTN_E_INVALID_ARG;
     if (ld < d.s_max || ld > (1ll << 38) || !(decay >= 0.f) || decay > 3.4e38f) return ATTN_E_INVALID_ARG;
     // the sums may take the place of what they add to, but not overlap it
     // otherwise, nor the births
@@ -64,7 +65,11 @@ int key_weights(attn_plan_t plan, const void *q, const void *k, long long k_stri
 
     p.qtile = plan->kw_qtile;
     CUtensorMap tm_q, tm_k;
-    int rc = encode_q_map(&tm_q, q, d.Hq, d.D, d.G, p.qtile);
+    // The maps end where the buffers end.  With an open extent a box that began
+    // before the first row of a short K (67 rows, 29 KB before the end of their
+    // mapping) touched addresses past it: an extent must not claim what is not
+    // there.
+    int rc = encode_q_map(&tm_q, q, d.Hq, d.D, d.G, p.qtile, T_q > 0 ? T_q : 1);
     if (rc != ATTN_OK) return rc;
     if (pg) {
         // pages a whole number of token rows apart: one row index per key
@@ -75,7 +80,7 @@ int key_weights(attn_plan_t plan, const void *q, const void *k, long long k_stri
                          : encode_paged_map(&tm_k, k, d.Hkv, d.D, pg->page_size, pg->num_pages, k_stride,
                                             pg->page_stride);
     } else {
-        rc = encode_kv_map(&tm_k, k, d.Hkv, d.D, 128, k_stride);
+        rc = encode_kv_map(&tm_k, k, d.Hkv, d.D, 128, k_stride, T_kv > 0 ? T_kv : 1);
     }
     if (rc != ATTN_OK) return rc;
     const cudaError_t e = launch_key_weights_tc(p, kw, tm_q, tm_k, plan->kw_columns, plan->kw_ctas, s);
@@ -84,18 +89,18 @@ int key_weights(attn_plan_t plan, const void *q, const void *k, long long k_stri
 
 }  // namespace
 
-ATTN_EXPORT int attn_key_weights(attn_plan_t plan, const void *q, const void *k, int64_t k_token_stride,
-                                 const int32_t *cu_q, const int32_t *cu_k, const float *lse, float decay,
+ATTN_EXPORT int attn_key_weights(attn_plan_t plan, const void *q, int64_t T_q, const void *k, int64_t k_token_stride,
+                                 int64_t T_kv, const int32_t *cu_q, const int32_t *cu_k, const float *lse, float decay,
                                  const float *weight_in, float *weight_out, int64_t ld, const int32_t *seen,
                                  int32_t *born, void *stream) {
     if (!plan || !live(plan)) return ATTN_E_BAD_PLAN;
     const long long packed = (long long)plan->d.Hkv * plan->d.D;
     if (k_token_stride < packed || k_token_stride % 8 != 0 || k_token_stride > (1ll << 38)) return ATTN_E_INVALID_ARG;
-    return key_weights(plan, q, k, k_token_stride, nullptr, cu_q, cu_k, lse, decay, weight_in, weight_out, ld, seen,
+    return key_weights(plan, q, T_q, k, k_token_stride, T_kv, nullptr, cu_q, cu_k, lse, decay, weight_in, weight_out, ld, seen,
                        born, stream);
 }
 
-ATTN_EXPORT int attn_key_weights_paged(attn_plan_t plan, const void *q, const void *k_cache, int64_t page_stride,
+ATTN_EXPORT int attn_key_weights_paged(attn_plan_t plan, const void *q, int64_t T_q, const void *k_cache, int64_t page_stride,
                                        int64_t token_stride, int page_size, int num_pages, const int32_t *block_table,
                                        int bt_stride, const int32_t *cu_q, const int32_t *cu_k, const float *lse,
                                        float decay, const float *weight_in, float *weight_out, int64_t ld,
@@ -104,6 +109,6 @@ ATTN_EXPORT int attn_key_weights_paged(attn_plan_t plan, const void *q, const vo
     const int rc = check_paging(plan, page_stride, token_stride, page_size, num_pages, block_table, bt_stride);
     if (rc != ATTN_OK) return rc;
     const Paging pg{block_table, bt_stride, page_size, num_pages, page_stride};
-    return key_weights(plan, q, k_cache, token_stride, &pg, cu_q, cu_k, lse, decay, weight_in, weight_out, ld, seen,
+    return key_weights(plan, q, T_q, k_cache, token_stride, 0, &pg, cu_q, cu_k, lse, decay, weight_in, weight_out, ld, seen,
                        born, stream);
 }

@@ -216,13 +216,14 @@ struct Walker {
         set(p);
         return true;
     }
-    // first key of sub-tile u, or -1 if the sequence ends before it; where its
-    // box starts (packed K: moved back to end with the sequence, so that no
-    // load passes the last key of a buffer)
+    // first key of sub-tile u, or -1 if the sequence ends before it
     __device__ int sub_key(int u) const {
         const int j = kt * kItemKeys + u * kSubKeys;
         return j < s.Lk ? j : -1;
     }
+    // where the box of packed K starts, in keys from the sequence's first (maybe
+    // before it): moved back to end with the sequence, but not before row 0
+    __device__ int packed_start(int j0) const { return max(min(j0, s.Lk - kSubKeys), -s.k0); }
 };
 
 // ------------------------------------------------------------ kernel
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                     __syncwarp();
                     if (lane < L::kHalves)
                         tma_load_3d(dst + lane * (kSubKeys * 128), &tm_k, &k_full[ks], lane * 64, it.hk,
-                                    it.s.k0 + min(j0, it.s.Lk - kSubKeys), pol_k);
+                                    it.s.k0 + it.packed_start(j0), pol_k);
                 }
                 ++nk;
                 if (++ks == KS) {
@@ -539,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
             if (n == 0 && !writes) continue;
             const int j0 = it.sub_key(u);
             const bool live = j0 >= 0;
-            const int key = (PAGED ? j0 : min(j0, it.s.Lk - kSubKeys)) + lane_key;
+            const int key = (PAGED ? j0 : it.packed_start(j0)) + lane_key;
             const bool mine = writes && live && key >= j0 && key < it.s.Lk;
             const int old = it.s.Lk - it.s.Lq;                   // keys below it were there before
             const long long at = ((long long)it.b * p.Hkv + it.hk) * kw.ld + key;

@@ -59,6 +59,6 @@ int encode_kv_map(CUtensorMap *map, const void *base, int Hkv, int D, int block_
                   long long rows = 0x7fffffff);
 int encode_paged_map(CUtensorMap *map, const void *base, int Hkv, int D, int page_size, int num_pages,
                      long long token_stride, long long page_stride);
-int encode_q_map(CUtensorMap *map, const void *base, int Hq, int D, int G, int qtile);
+int encode_q_map(CUtensorMap *map, const void *base, int Hq, int D, int G, int qtile, long long rows = 0x7fffffff);
 
 }  // namespace vgqa

@@ -238,15 +238,16 @@ PyObject *key_weights(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (given(a[3])) {
             const CacheArgs c(p, a[2], nullptr, a[3]);
             return call([&] {
-                return f_weights_paged(p.plan, q, c.k, c.page_stride, c.token_stride, c.page_size, c.num_pages, c.table,
+                return f_weights_paged(p.plan, q, T, c.k, c.page_stride, c.token_stride, c.page_size, c.num_pages, c.table,
                                        c.bt_stride, cu_q, cu_k, lse, (float)decay, in, out, ld, seen, born, stream);
             });
         }
         const at::Tensor &k0 = tensor(a[2], "k", at::kBFloat16, p.dev);
         long long ks;
-        void *k = heads(a[2], "k", at::kBFloat16, p.dev, k0.dim() ? k0.size(0) : 0, p.Hkv, p.D, &ks);
+        const long long T_kv = k0.dim() ? k0.size(0) : 0;
+        void *k = heads(a[2], "k", at::kBFloat16, p.dev, T_kv, p.Hkv, p.D, &ks);
         return call([&] {
-            return f_weights(p.plan, q, k, ks, cu_q, cu_k, lse, (float)decay, in, out, ld, seen, born, stream);
+            return f_weights(p.plan, q, T, k, ks, T_kv, cu_q, cu_k, lse, (float)decay, in, out, ld, seen, born, stream);
         });
     });
 }
