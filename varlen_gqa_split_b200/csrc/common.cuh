@@ -392,6 +392,30 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t *p) {
     return v;
 }
 
+// Programmatic dependent launch: wait until the work before this kernel in the
+// stream is complete and visible, then (`release`) let the next kernel's blocks
+// start, which wait in turn.  A kernel that writes lengths does not release.
+__device__ __forceinline__ void dependent_start(bool release = true) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (release) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// load_lengths by plain loads, for kernels that begin with dependent_start()
+__device__ __forceinline__ bool read_lengths(const Params &p, int b, bool report, int &q0, int &Lq, int &k0, int &Lk) {
+    q0 = p.cu_q[b];
+    k0 = p.cu_k[b];
+    Lq = p.cu_q[b + 1] - q0;
+    Lk = p.cu_k[b + 1] - k0;
+    uint32_t bad = 0;
+    if (q0 < 0 || k0 < 0 || Lq < 0 || Lk < 0) bad |= ATTN_DEV_ERR_OFFSETS;
+    else {
+        if (Lq > p.max_q) bad |= ATTN_DEV_ERR_Q_TOO_LONG;
+        if (Lk > p.s_max) bad |= ATTN_DEV_ERR_K_TOO_LONG;
+    }
+    if (bad && report) atomicOr(p.err, bad);
+    return bad == 0;
+}
+
 // named barrier over `nthreads` threads (a subset of the block)
 __device__ __forceinline__ void named_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");

@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t order_of(float w, bool fixed) {
 
 // this block's sequence lengths: only cu_k counts
 __device__ __forceinline__ bool key_length(const Params &p, int b, bool report, int &Lk) {
-    const int k0 = __ldg(p.cu_k + b), k1 = __ldg(p.cu_k + b + 1);
+    const int k0 = p.cu_k[b], k1 = p.cu_k[b + 1];
     Lk = k1 - k0;
     const uint32_t bad = (k0 < 0 || Lk < 0) ? ATTN_DEV_ERR_OFFSETS : Lk > p.s_max ? ATTN_DEV_ERR_K_TOO_LONG : 0u;
     if (bad && report) atomicOr(p.err, bad);
@@ -108,7 +108,7 @@ __device__ void write_offsets(const Params &p, const Evict &e, int *scratch) {
     for (int b0 = 0; b0 < p.B_max; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         int c = 0, Lk;
-        if (b < p.B_max && key_length(p, b, true, Lk)) c = min(Lk, max(0, __ldg(e.keep + b)));
+        if (b < p.B_max && key_length(p, b, true, Lk)) c = min(Lk, max(0, e.keep[b]));
         int total;
         const int s = block_scan(c, scratch, total);
         if (b < p.B_max) e.cu_out[b + 1] = carry + s;
@@ -172,12 +172,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) evict_kernel(const Par
     cg::cluster_group cluster = cg::this_cluster();
     const int CS = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int unit = blockIdx.x / CS, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    dependent_start(false);
     if (unit == p.B_max * p.Hkv) {        // the extra cluster
         if (rank == 0) write_offsets(p, e, sh.scratch);
         return;
     }
     const int b = unit / p.Hkv, hk = unit % p.Hkv;
-    const int keep = __ldg(e.keep + b), seen = __ldg(e.seen + b);   // on their way with the length
+    const int keep = e.keep[b], seen = e.seen[b];   // on their way with the length
     int n;
     if (!key_length(p, b, false, n)) return;
     const int c = min(n, max(0, keep));
@@ -514,7 +515,7 @@ cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
     e.slice_words = slice_words(p.s_max, cs);
     const size_t fixed = sizeof(Head) + bits_bytes(p.s_max, cs), ranks = (size_t)e.slice_words * 32 * 4;
     e.cached = fixed + ranks <= (size_t)kMaxSmem ? e.slice_words * 32 : 0;
-    return launch_grid(evict_kernel, dim3((unsigned)((p.B_max * p.Hkv + 1) * cs)), dim3(kThreads),
+    return launch_dependent(evict_kernel, dim3((unsigned)((p.B_max * p.Hkv + 1) * cs)), dim3(kThreads),
                             fixed + (e.cached ? ranks : 0), stream, cs > 1 ? cs : 0, p, e);
 }
 

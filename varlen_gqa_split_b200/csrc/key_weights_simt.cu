@@ -104,8 +104,11 @@ __global__ void __launch_bounds__(kKeys) key_weights_simt_kernel(const Params p,
 
 cudaError_t launch_key_weights_simt(const Params &p, const KeyWeights &kw, cudaStream_t stream) {
     const dim3 grid((p.s_max + kKeys - 1) / kKeys, p.Hkv, p.B_max);
-    return launch_grid(p.D == 64 ? key_weights_simt_kernel<64> : key_weights_simt_kernel<128>, grid, dim3(kKeys), 0,
-                            stream, 0, p, kw);
+    if (p.D == 64)
+        key_weights_simt_kernel<64><<<grid, kKeys, 0, stream>>>(p, kw);
+    else
+        key_weights_simt_kernel<128><<<grid, kKeys, 0, stream>>>(p, kw);
+    return cudaGetLastError();
 }
 
 }  // namespace vgqa

@@ -88,7 +88,7 @@ __device__ __forceinline__ SeqInfo seq_info(const Params &p, int b, bool report)
     SeqInfo s;
     s.nkt = s.nrt = s.ksat = 0;
     s.tot = 0;
-    if (!load_lengths(p, b, report, s.q0, s.Lq, s.k0, s.Lk) || s.Lk == 0) return s;
+    if (!read_lengths(p, b, report, s.q0, s.Lq, s.k0, s.Lk) || s.Lk == 0) return s;
     s.nkt = (s.Lk + kItemKeys - 1) / kItemKeys;
     s.nrt = (s.Lq + p.qtile - 1) / p.qtile;
     if (s.nrt <= 1) {                     // decode; or no query: its items only pass on what they had
@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
         tc::tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
         tc::tmem_relinquish();
     }
+    dependent_start();
     Share sh;
     const bool has_work = block_share(p, tid, scan, found, sh);
     tc::fence_before_sync();
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
                     const bool row = tok[i] >= 0 && t0 + tok[i] >= 0;
-                    v[i] = row ? __ldg(src + off[i]) : -INFINITY;
+                    v[i] = row ? src[off[i]] : -INFINITY;
                     skip |= row && v[i] == -INFINITY;
                 }
                 skip = __any_sync(0xffffffffu, skip);
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
             }
             if (all && mine) {
                 kw.w_out[at] = kw.decay * before + total;
-                if (kw.born && key >= old) kw.born[at] = __ldg(kw.seen + it.b) - (it.s.Lk - key);
+                if (kw.born && key >= old) kw.born[at] = kw.seen[it.b] - (it.s.Lk - key);
             }
         } while (it.next(p));
         if (!ok) *stop = 1;
@@ -701,7 +702,7 @@ cudaError_t launch_key_weights_tc(const Params &p, const KeyWeights &kw, const C
     Kernel fn;
     size_t smem;
     pick(p.D, columns, p.block_table != nullptr, fn, smem);
-    return launch_grid(fn, dim3(ctas), dim3(kThreads), smem, stream, 0, tm_q, tm_k, p, kw);
+    return launch_dependent(fn, dim3(ctas), dim3(kThreads), smem, stream, 0, tm_q, tm_k, p, kw);
 }
 
 }  // namespace vgqa

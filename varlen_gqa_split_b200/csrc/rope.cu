@@ -63,20 +63,21 @@ Shape shape_of(long long n_tok, int heads, int groups, int n, int most) {
 }
 
 // the cosines and sines of tokens [t0, t0 + nt): cs[token][pair]
-__device__ __forceinline__ void fill_factors(const RopeTable &tab, float2 *cs, const int32_t *__restrict__ pos,
+__device__ __forceinline__ void fill_factors(const RopeTable &tab, float2 *cs, const int32_t *pos,
                                              long long ps, long long t0, int nt, float sign) {
     for (int i = threadIdx.x; i < nt * tab.n; i += blockDim.x) {
         const int t = i / tab.n, pr = i - t * tab.n;
-        cs[i] = rope_cos_sin(tab, pr, __ldg(pos + tab.axis[pr] * ps + t0 + t), sign);
+        cs[i] = rope_cos_sin(tab, pr, pos[tab.axis[pr] * ps + t0 + t], sign);
     }
 }
 
 template <typename T, int V, bool HALF>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     rope_kernel(const __grid_constant__ RopeTable tab, const T *x, long long xs, long long n_tok, int H, int D,
-                const int32_t *__restrict__ pos, long long ps, float sign, T *out, long long os, int groups, int lanes,
+                const int32_t *pos, long long ps, float sign, T *out, long long os, int groups, int lanes,
                 int tokens) {
     extern __shared__ float2 cs[];
+    dependent_start();
     const int n = tab.n;
     const long long t0 = (long long)blockIdx.x * tokens;
     const int nt = (int)min((long long)tokens, n_tok - t0);
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     using T = __nv_bfloat16;
     using W = Vec<T, V>;
     extern __shared__ float2 cs[];            // [tokens][n], then [tokens] cache offsets, [tokens] (sequence, key)
+    dependent_start();
     const int n = tab.n, tokens = ap.tokens, tid = threadIdx.x, D = p.D;
     long long *slot = reinterpret_cast<long long *>(cs + tokens * n);
     int2 *owner = reinterpret_cast<int2 *>(slot + tokens);
@@ -166,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     __syncthreads();
     for (int s = tid; s < p.B_max; s += blockDim.x) {
         int q0, Lq, k0, Lk;
-        if (!load_lengths(p, s, blockIdx.x == 0, q0, Lq, k0, Lk)) continue;
+        if (!read_lengths(p, s, blockIdx.x == 0, q0, Lq, k0, Lk)) continue;
         const int lo = (int)max(0ll, q0 - t0), hi = (int)min((long long)nt, q0 + Lq - t0);
         for (int i = lo; i < hi; ++i) owner[i] = make_int2(s, (int)(Lk - Lq + (t0 + i - q0)));
     }
@@ -241,7 +243,7 @@ cudaError_t launch_rope(const attn_rope_s &r, const void *x, long long xs, long 
     if (sh.blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     const size_t smem = (size_t)sh.tokens * r.tab.n * sizeof(float2);
     auto *fn = r.layout == ATTN_ROPE_HALF ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
-    return launch_grid(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, r.tab,
+    return launch_dependent(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, r.tab,
                             static_cast<const T *>(x), xs, n_tok, H, r.D, pos, ps, grad ? -1.f : 1.f,
                             static_cast<T *>(out), os, sh.groups, sh.lanes, sh.tokens);
 }
@@ -256,7 +258,7 @@ cudaError_t launch_append(const RopeTable &tab, bool half, const Params &p, Appe
     ap.tokens = sh.tokens;
     const size_t smem = (size_t)sh.tokens * (tab.n * sizeof(float2) + sizeof(long long) + sizeof(int2));
     auto *fn = half ? append_kernel<V, true> : append_kernel<V, false>;
-    return launch_grid(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, tab, p, ap);
+    return launch_dependent(fn, dim3((unsigned)sh.blocks), dim3(sh.threads), smem, s, 0, tab, p, ap);
 }
 
 }  // namespace
