@@ -25,9 +25,9 @@
 //   4. the moves: pair i finds its place and its key by binary search in
 //      those counts, and 16 bytes a thread go from row to row.
 // Small cuts take the latency of those steps (64 sequences x 8 heads of 1044
-// keys cut to 1024: 13.6 us; 8 heads of 32768 keys to 2048: 19.9), large ones
+// keys cut to 1024: 13.2 us; 8 heads of 32768 keys to 2048: 18.9), large ones
 // the bandwidth of the moved rows (64 x 8 heads of up to 8192 keys to 1024:
-// 75.5 us, 86% of the measured HBM bandwidth).
+// 78.5 us, 82% of the measured HBM bandwidth).
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -508,7 +508,7 @@ namespace {
 
 cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
     // A cluster per unit: as many blocks as fill the device, but no slice
-    // under 1024 keys (8 units of 32768 keys: 8 blocks each 19.9 us, 4 29.4)
+    // under 1024 keys (8 units of 32768 keys: 8 blocks each 18.9 us, 4 29.4 before the last steps)
     const long long units = (long long)p.B_max * p.Hkv;
     int cs = 1;
     while (cs < kMaxCluster && units * cs * 2 <= 148 * kBlocksPerSm && p.s_max >= 2048 * cs) cs *= 2;

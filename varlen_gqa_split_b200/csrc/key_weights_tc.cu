@@ -18,9 +18,9 @@
 // parts, 256 sums each, are added in block order by whichever block finishes
 // last.  Decode has one row tile per item: no cuts, K streams through.
 //
-// Measured: 64 ragged sequences of a decode step (8 KV heads, 554 MB) 90.7 us,
-// 93% of the measured HBM bandwidth; 2 x 1025..2048 tokens over 24k..32k keys,
-// 64 heads, 1.67 ms, 0.51 of the measured tensor rate: the exponentials need
+// Measured: 64 ragged sequences of a decode step (8 KV heads, 554 MB) 91 to 94
+// us, 90 to 93% of the measured HBM bandwidth; 2 x 1025..2048 tokens over 24k..32k keys,
+// 64 heads, 1.67 to 1.79 ms, 0.5 of the measured tensor rate: the exponentials need
 // 1.2 ms of the special-function unit (79% busy).
 //
 // Warps: 0-15 epilogue (warp w: sub-tile w / 4 mod 2, lanes 32 (w mod 4), and
