@@ -96,7 +96,7 @@ __device__ __forceinline__ void merge_few(const Params &p, const int *slots, int
 // merging, each of the unit's n * S combine blocks adds 1 to the count again;
 // the last one resets it for the next call.
 template <int D>
-__global__ void __launch_bounds__(128, 4) combine_slots_kernel(const Params p, const int C, const int S) {
+__device__ __forceinline__ void combine_unit(const Params &p, const int C, const int S) {
     constexpr int kCols = D / 4;
     constexpr int kT = 128;
     constexpr int kBatch = 12;             // loads in flight per thread (register budget)
@@ -109,9 +109,6 @@ __global__ void __launch_bounds__(128, 4) combine_slots_kernel(const Params p, c
     const int sub = blockIdx.x % S;
     const int c = (blockIdx.x / S) >> 1, k = (blockIdx.x / S) & 1;
     const long long ROWS = p.rows_per_block;     // rows of one partial slot
-    // the next call's split kernel may launch now; it waits for this grid to
-    // complete before it reads anything
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     Share sh;
     if (!block_share(p, c, C, tid, kT, false, scan, first, sh)) return;
@@ -253,7 +250,19 @@ __global__ void __launch_bounds__(128, 4) combine_slots_kernel(const Params p, c
     if (tid == 0 && atomicAdd(p.done + u, 1u) == parts_done + (uint32_t)(nb - 1)) p.done[u] = 0u;
 }
 
-
+template <int D>
+__global__ void __launch_bounds__(128, 4) combine_slots_kernel(const Params p, const int C, const int S) {
+    // the kernel that follows may launch now; it waits for this grid to
+    // complete before it reads anything
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    combine_unit<D>(p, C, S);
+    // That wait covers this grid alone, and the parts waited for above are
+    // those of cut units: the split kernel may still be writing whole units.
+    // Block 0, its merge done, stays until the split grid is complete, so that
+    // this grid's completion stands for both.  (One block: the others' places
+    // go to the blocks that still have a unit to merge.)
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 }  // namespace
 

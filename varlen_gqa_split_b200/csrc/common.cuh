@@ -392,9 +392,10 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t *p) {
     return v;
 }
 
-// Programmatic dependent launch: wait until the work before this kernel in the
-// stream is complete and visible, then (`release`) let the next kernel's blocks
-// start, which wait in turn.  A kernel that writes lengths does not release.
+// Programmatic dependent launch: wait until the kernel before this one in the
+// stream is complete and what it wrote visible (and with it all work before
+// that: no kernel of the library completes before its own predecessor), then
+// (`release`) let the next kernel's blocks start, which wait in turn.  A kernel that writes lengths does not release.
 __device__ __forceinline__ void dependent_start(bool release = true) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (release) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -13,7 +13,9 @@ struct Params;
 // in clusters of `cluster` blocks where it is not zero.  EVERY kernel launched
 // with it calls dependent_start() before its first read of global memory, and
 // reads what the kernel before it may have written by plain loads (a read-only
-// load may be moved ahead of the wait).  Takes 0.5 to 1 us off a small call
+// load may be moved ahead of the wait).  The wait covers the grid just before
+// it in the stream alone, so every grid of the library that lets its successor
+// start early waits for its own predecessor before it completes.  Takes 0.5 to 1 us off a small call
 // that follows another (64 tokens rotated 3.45 -> 2.9 us).
 template <typename... A>
 cudaError_t launch_dependent(void (*fn)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster,
