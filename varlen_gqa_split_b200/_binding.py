@@ -142,9 +142,9 @@ def merge_lse(outs, lses, cu_q, out=None, lse=None, stream=None):
     if cu_q.dtype != torch.int32 or not cu_q.is_cuda or not cu_q.is_contiguous() or cu_q.dim() != 1:
         raise ValueError("cu_q must be a contiguous int32 CUDA tensor")
     if out is None:
-        out = torch.empty(T_q, Hq, D, dtype=torch.bfloat16, device=outs.device)
+        out = _made(stream, torch.empty, T_q, Hq, D, dtype=torch.bfloat16, device=outs.device)
     if lse is None:
-        lse = torch.empty(T_q, Hq, dtype=torch.float32, device=outs.device)
+        lse = _made(stream, torch.empty, T_q, Hq, dtype=torch.float32, device=outs.device)
     if out.dtype != torch.bfloat16 or tuple(out.shape) != (T_q, Hq, D) or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor [T_q, Hq, D]")
     if lse.dtype != torch.float32 or tuple(lse.shape) != (T_q, Hq) or not lse.is_contiguous():
@@ -177,6 +177,19 @@ def _stream_ptr(stream) -> int:
     if _raw_stream is not None:
         return _raw_stream(_raw_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+def _made(stream, make, *args, **kw):
+    """A result that the caller did not pass.  It is made, and filled, on the
+    stream that the call runs on: a fill on another one could come after the
+    kernel, and the allocator could hand the memory of a dropped result to that
+    other stream while the kernel still writes it."""
+    if stream is None:
+        return make(*args, **kw)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
 
 
 def rope_table(n_pairs, sections=None, *, base=10000.0, restart=False):
@@ -235,7 +248,7 @@ class Rope:
         if self._h is None:
             raise AttnError(-3, "attn_rope_apply")
         if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+            out = _made(stream, torch.empty_like, x, memory_format=torch.contiguous_format)
         rc = _marshal.rope_apply(self._h.value, self.D, self.n_axes, _raw_device(), x, pos, out, grad,
                                  _stream_ptr(stream))
         if rc:
@@ -301,7 +314,7 @@ class Plan:
         fused [T, 2, Hkv, D] cache), which go through attn_run_strided;
         cu_q / cu_k int32 CUDA tensors with B_max + 1 entries; out / lse are
         allocated when not given (pass them for graph capture)."""
-        out, lse = self._check_common(q, cu_q, cu_k, out, lse, "attn_run")
+        out, lse = self._check_common(q, cu_q, cu_k, out, lse, "attn_run", stream)
         i = self.info
         for name, t in (("k", k), ("v", v)):
             if t.dtype != torch.bfloat16 or not t.is_cuda:
@@ -334,7 +347,7 @@ class Plan:
         sequence b in key order (n >= ceil(s_max / page_size), row stride
         free); cu_k supplies the key lengths only.  Goes through
         attn_run_paged."""
-        out, lse = self._check_common(q, cu_q, cu_k, out, lse, "attn_run_paged")
+        out, lse = self._check_common(q, cu_q, cu_k, out, lse, "attn_run_paged", stream)
         i = self.info
         shape = None
         for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
@@ -378,7 +391,7 @@ class Plan:
             if q_out is not None:
                 raise ValueError("q_out without q")
         elif q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = _made(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
         rp = n_axes = 0
         if rope is not None:
             if rope._h is None:
@@ -402,8 +415,8 @@ class Plan:
         if out is None:
             like = weight_in if weight_in is not None else born
             i = self.info
-            out = torch.zeros((i["B_max"], i["Hkv"], i["s_max"] if like is None else like.shape[-1]),
-                              dtype=torch.float32, device=q.device)
+            out = _made(stream, torch.zeros, (i["B_max"], i["Hkv"], i["s_max"] if like is None else like.shape[-1]),
+                        dtype=torch.float32, device=q.device)
         rc = _marshal.key_weights(self._args, q, k, block_table, cu_q, cu_k, lse, weight_in, decay, out, seen, born,
                                   _stream_ptr(stream))
         if rc:
@@ -451,14 +464,14 @@ class Plan:
         if born_out is None:
             born_out = born
         if cu_k_out is None:
-            cu_k_out = torch.empty_like(cu_k)
+            cu_k_out = _made(stream, torch.empty_like, cu_k)
         rc = _marshal.evict_paged(self._args, weight, born, seen, keep, k_cache, v_cache, block_table, cu_k, sink, recent,
                                   weight_out, born_out, cu_k_out, _stream_ptr(stream))
         if rc:
             _check(rc, "attn_evict_paged")
         return weight_out, born_out, cu_k_out
 
-    def _check_common(self, q, cu_q, cu_k, out, lse, where):
+    def _check_common(self, q, cu_q, cu_k, out, lse, where, stream):
         if self._h is None:
             raise AttnError(-5, where)
         i = self.info
@@ -470,9 +483,9 @@ class Plan:
             if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() != i["B_max"] + 1:
                 raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of B_max+1 entries")
         if out is None:
-            out = torch.empty_like(q)
+            out = _made(stream, torch.empty_like, q)
         if lse is None:
-            lse = torch.empty(q.shape[0], i["Hq"], dtype=torch.float32, device=q.device)
+            lse = _made(stream, torch.empty, q.shape[0], i["Hq"], dtype=torch.float32, device=q.device)
         if out.dtype != torch.bfloat16 or out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be a contiguous bf16 tensor shaped like q")
         if lse.dtype != torch.float32 or lse.shape != (q.shape[0], i["Hq"]) or not lse.is_contiguous():
