@@ -111,3 +111,14 @@ def test_calls_behind_attention_read_its_results(B, Hq, Hkv, lq, lens, paged):
             for got, want in zip(step(i, lambda: None), refs[i]):
                 assert torch.equal(got.view(torch.uint8), want.view(torch.uint8)), (rep, i)
     assert plan.check_error() == 0
+
+
+def test_programmatic_dependents_read_by_plain_loads():
+    """Read-only loads (ld.global.nc) may be moved ahead of the wait and promise
+    that nothing is written while the kernel lives, and a programmatic dependent
+    lives while its predecessor still writes."""
+    csrc = os.path.join(ROOT, "varlen_gqa_split_b200", "csrc")
+    for path in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
+        text = re.sub(r"//[^\n]*|/\*.*?\*/", "", open(path).read(), flags=re.S)
+        if path.endswith(".cuh") or "ProgrammaticStreamSerialization" in text or "launch_dependent(" in text:
+            assert not re.search(r"__ldg\s*\(|ld\.global(\.\w+)*\.nc\b|__restrict__", text), os.path.basename(path)

@@ -143,7 +143,7 @@ __device__ __forceinline__ void combine_unit(const Params &p, const int C, const
     // wait for the unit's n parts, each published by done_per_part release
     // adds (the acquire pairs with them); p.stall adds parts that never come
     // (a test hook, 0 otherwise), so that the bounded wait below runs out
-    const uint32_t parts_done = (uint32_t)(n * p.done_per_part) + __ldg(p.stall);
+    const uint32_t parts_done = (uint32_t)(n * p.done_per_part) + *p.stall;
     if (tid == 0) {
         int ok = 1;
         if (ld_acquire_gpu(p.done + u) < parts_done) {

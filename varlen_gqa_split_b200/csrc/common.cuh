@@ -42,13 +42,15 @@ __device__ __forceinline__ int live_chunks(int Lk, int chunk) {
 // skipped.  The same test runs in every kernel that touches the sequence.
 // spec: a speculative read made before the kernel has waited for the one it
 // depends on (the value may still change); it goes to L2 only, so that no
-// line of cu_seqlens stays in L1 for the later, real reads to hit.
+// line of cu_seqlens stays in L1 for the later, real reads to hit.  The real
+// reads are plain loads, which stay behind the wait: the kernel before may
+// have written the lengths (eviction does).
 __device__ __forceinline__ bool load_lengths(const Params &p, int b, bool report,
                                              int &q0, int &Lq, int &k0, int &Lk, bool spec = false) {
-    q0 = spec ? __ldcg(p.cu_q + b) : __ldg(p.cu_q + b);
-    const int q1 = spec ? __ldcg(p.cu_q + b + 1) : __ldg(p.cu_q + b + 1);
-    k0 = spec ? __ldcg(p.cu_k + b) : __ldg(p.cu_k + b);
-    const int k1 = spec ? __ldcg(p.cu_k + b + 1) : __ldg(p.cu_k + b + 1);
+    q0 = spec ? __ldcg(p.cu_q + b) : p.cu_q[b];
+    const int q1 = spec ? __ldcg(p.cu_q + b + 1) : p.cu_q[b + 1];
+    k0 = spec ? __ldcg(p.cu_k + b) : p.cu_k[b];
+    const int k1 = spec ? __ldcg(p.cu_k + b + 1) : p.cu_k[b + 1];
     Lq = q1 - q0;
     Lk = k1 - k0;
     uint32_t bad = 0;
@@ -62,8 +64,9 @@ __device__ __forceinline__ bool load_lengths(const Params &p, int b, bool report
 }
 
 // Paged K/V: the page holding key j of sequence b, from the block table, in
-// two steps so that the table read can overlap a wait: page_entry() issues
-// the read, page_checked() validates the value.  An entry outside
+// two steps so that the table read can overlap a barrier wait: page_entry()
+// issues the read (no read-only load: the kernel before may have written the
+// table), page_checked() validates the value.  An entry outside
 // [0, num_pages) raises ATTN_DEV_ERR_PAGE and gives num_pages, a page past
 // the cache: tensor-map loads of it fill zeros and the CUDA-core path skips
 // it, so a bad table never reads outside the cache.
@@ -71,7 +74,7 @@ __device__ __forceinline__ int page_entry(const Params &p, int b, int j) {
     // volatile: stays ahead of the (volatile) barrier wait that follows it,
     // so the read is in flight during the wait
     int pg;
-    asm volatile("ld.global.nc.b32 %0, [%1];"
+    asm volatile("ld.global.b32 %0, [%1];"
                  : "=r"(pg)
                  : "l"(p.block_table + (long long)b * p.bt_stride + (j >> p.page_shift)));
     return pg;
@@ -399,22 +402,6 @@ __device__ __forceinline__ uint32_t ld_acquire_gpu(const uint32_t *p) {
 __device__ __forceinline__ void dependent_start(bool release = true) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (release) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// load_lengths by plain loads, for kernels that begin with dependent_start()
-__device__ __forceinline__ bool read_lengths(const Params &p, int b, bool report, int &q0, int &Lq, int &k0, int &Lk) {
-    q0 = p.cu_q[b];
-    k0 = p.cu_k[b];
-    Lq = p.cu_q[b + 1] - q0;
-    Lk = p.cu_k[b + 1] - k0;
-    uint32_t bad = 0;
-    if (q0 < 0 || k0 < 0 || Lq < 0 || Lk < 0) bad |= ATTN_DEV_ERR_OFFSETS;
-    else {
-        if (Lq > p.max_q) bad |= ATTN_DEV_ERR_Q_TOO_LONG;
-        if (Lk > p.s_max) bad |= ATTN_DEV_ERR_K_TOO_LONG;
-    }
-    if (bad && report) atomicOr(p.err, bad);
-    return bad == 0;
 }
 
 // named barrier over `nthreads` threads (a subset of the block)

@@ -88,7 +88,7 @@ __device__ __forceinline__ SeqInfo seq_info(const Params &p, int b, bool report)
     SeqInfo s;
     s.nkt = s.nrt = s.ksat = 0;
     s.tot = 0;
-    if (!read_lengths(p, b, report, s.q0, s.Lq, s.k0, s.Lk) || s.Lk == 0) return s;
+    if (!load_lengths(p, b, report, s.q0, s.Lq, s.k0, s.Lk) || s.Lk == 0) return s;
     s.nkt = (s.Lk + kItemKeys - 1) / kItemKeys;
     s.nrt = (s.Lq + p.qtile - 1) / p.qtile;
     if (s.nrt <= 1) {                     // decode; or no query: its items only pass on what they had

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     __syncthreads();
     for (int s = tid; s < p.B_max; s += blockDim.x) {
         int q0, Lq, k0, Lk;
-        if (!read_lengths(p, s, blockIdx.x == 0, q0, Lq, k0, Lk)) continue;
+        if (!load_lengths(p, s, blockIdx.x == 0, q0, Lq, k0, Lk)) continue;
         const int lo = (int)max(0ll, q0 - t0), hi = (int)min((long long)nt, q0 + Lq - t0);
         for (int i = lo; i < hi; ++i) owner[i] = make_int2(s, (int)(Lk - Lq + (t0 + i - q0)));
     }

@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
     float *ms = ored + kConsumerWarps * ROWS * OLD;           // [4][ROWS]
     float *lsum = ms + kConsumerWarps * ROWS;                  // [4][ROWS]
 
-    // Q^T fragments (B operand of S^T): row n = nt*8 + grp, d = 16ks + 2tig (+8)
+    // Q^T fragments (B operand of S^T): row n = nt*8 + grp, d = 16ks + 2tig (+8);
+    // plain loads: the kernel before may have written the queries
     auto load_q = [&](const Segment &sg, uint32_t (&qf)[NT][KS][2]) {
         const int R = G * sg.s.Lq;
 #pragma unroll
@@ -268,8 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
                 p.q + ((long long)(sg.s.q0 + (ok ? r / G : 0)) * p.Hq + sg.hk * G + (ok ? r % G : 0)) * D);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                qf[nt][ks][0] = ok ? __ldg(qp + (ks * 16 + 2 * tig) / 2) : 0u;
-                qf[nt][ks][1] = ok ? __ldg(qp + (ks * 16 + 8 + 2 * tig) / 2) : 0u;
+                qf[nt][ks][0] = ok ? qp[(ks * 16 + 2 * tig) / 2] : 0u;
+                qf[nt][ks][1] = ok ? qp[(ks * 16 + 8 + 2 * tig) / 2] : 0u;
             }
         }
     };

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
                 // p.stall adds parts that never come (a test hook, 0
                 // otherwise), so that the bounded wait runs out
                 mu = unit_index(p, sg.b, sg.hk, sg.rt);
-                mneed = (uint32_t)((c - block_of(sg.Pu, sh.T, sh.Ce)) * kSoftWarps) + __ldg(p.stall);
+                mneed = (uint32_t)((c - block_of(sg.Pu, sh.T, sh.Ce)) * kSoftWarps) + *p.stall;
             }
             if constexpr (PAGED) prefetch_pages(p, sg.b, sg.s.Lk, lane, 32);
             if (!acquire()) return false;
