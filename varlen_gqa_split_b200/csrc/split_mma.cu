@@ -309,6 +309,26 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
 
+        // The box of a packed sequence of less than a tile starts before it, on
+        // rows of another one.  This warp zeroes its rows of them in V: their
+        // weights are 0, but 0 times a non-finite value would not be (rows
+        // before the buffer's first came as zeros).  The unit has this one
+        // tile.  (256 sequences of 40 keys, 8 KV heads: 36.5 -> 38.5 us a call;
+        // inside the loop it would cost every batch 1 to 2%, and a producer
+        // that waits for such a tile and zeroes costs 2% of a ragged batch with
+        // two such sequences.)
+        if (!PAGED && Lk < kBN && cur.s.k0 > 0 && mbar_wait(&full[s], phase, p.wait_ns) &&
+            !(meta[s].y & kMetaEmpty)) {
+            constexpr int kChunks = L::kHalves * 8, kStep = 32 / kChunks;     // 16-byte pieces of a row, rows at once
+            const int r0 = kbase + lane / kChunks, piece = lane % kChunks;
+            const uint32_t at = ring_base + s * L::kStageBytes + L::kTileBytes + (piece >> 3) * L::kRegion + r0 * 128 +
+                                (piece & 7) * 16;
+#pragma unroll
+            for (int i = 0; i < 16; i += kStep)
+                if (r0 + i < kBN - Lk && r0 + i >= kBN - Lk - cur.s.k0) st_shared_zero16(at + i * 128);
+            fence_proxy_async();                    // ahead of the stage's next load
+            __syncwarp();
+        }
         while (ok_run) {
             if (!mbar_wait(&full[s], phase, p.wait_ns)) {
                 atomicOr(p.err, ATTN_DEV_ERR_TIMEOUT);

@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
     uint64_t *o_free = o_done + 2;           // O read by the epilogue
     uint64_t *xbar = o_free + 1;             // [4] the two warps of a lane quarter exchanged a value
     uint64_t *drain = xbar + 4;              // all issued tensor-core work done
-    uint64_t *mg = drain + 1;                // fused merge: the other parts are published ([2]: alignment)
+    uint64_t *mg = drain + 1;                // fused merge: the other parts are published
+    uint64_t *lone = mg + 1;                 // a tile that the producer waits for itself has landed
     int4 *meta = reinterpret_cast<int4 *>(mg + 2);                            // [stages]
     UnitDesc *units = reinterpret_cast<UnitDesc *>(meta + stages);           // [kSegRing]
     float *xbuf = reinterpret_cast<float *>(units + kSegRing);               // [2][2 halves][128]
@@ -180,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
         for (int i = 0; i < 4; ++i) mbar_init(&xbar[i], 2);
         mbar_init(drain, 1);
         mbar_init(mg, 1);
+        mbar_init(lone, 1);
         *stop = 0;
         fence_barrier_init();
     }
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
         int s = 0, issued = 0;
         uint32_t phase = 0;
         int nseg = 0;                        // units begun
+        uint32_t lone_phase = 0;
         int nsub = 0;                        // tiles in the open stage (0: none open)
         int ks_a = 0, ks_b = 0;              // key starts of the open stage's tiles
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -329,13 +332,44 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
                 }
             } else {
                 if (nsub == 0 && !acquire()) return false;
-                if (leader) mbar_expect_tx(&full[s], L::kTileBytes);
-                __syncwarp(wmask);
+                // The box of a sequence of less than a tile starts before it, on
+                // rows of another one, whatever they hold: weight 0 times a
+                // non-finite value would not be 0.  The producer waits for such
+                // a tile (the only one of its unit) and zeroes those rows before
+                // the stage counts as full; softmax loops that did it took 2%
+                // longer on batches without such a sequence.  Rows before the
+                // buffer's first come as zeros.
                 const int row = sg.s.k0 + min(ks, sg.s.Lk - kBN);
-                if (lane < 2 * L::kHalves) {                        // lane: (K or V, D-half)
-                    const int tv = lane / L::kHalves, hf = lane % L::kHalves;
-                    tma_load_3d(ring + s * L::kStage + tv * L::kKvTile + hf * L::kKvRegion + nsub * L::kSubRows,
-                                tv ? &tm_v : &tm_k, &full[s], hf * 64, sg.hk, row, pol);
+                uint8_t *st = ring + s * L::kStage + nsub * L::kSubRows;
+                const int tv = lane / L::kHalves, hf = lane % L::kHalves;   // lane: (K or V, D-half)
+                if (sg.s.Lk < kBN && sg.s.k0 > 0) {
+                    if (leader) mbar_arrive_expect_tx(lone, L::kTileBytes);
+                    __syncwarp(wmask);
+                    if (lane < 2 * L::kHalves)
+                        tma_load_3d(st + tv * L::kKvTile + hf * L::kKvRegion, tv ? &tm_v : &tm_k, lone, hf * 64, sg.hk,
+                                    row, pol);
+                    if (!wait_all(lone, lone_phase)) {
+                        mbar_wait(lone, lone_phase);                // the copies land before the block leaves
+                        return false;
+                    }
+                    lone_phase ^= 1;
+                    constexpr int kChunks = 2 * L::kHalves * 8;     // 16-byte pieces of a row of K and V
+                    const int from = max(0, kBN - sg.s.Lk - sg.s.k0), n = kBN - sg.s.Lk - from;
+                    const uint32_t at = smem_u32(st) + from * 128;
+#pragma unroll 1
+                    for (int i = lane; i < n * kChunks; i += 32) {
+                        const int r = i / kChunks, o = i % kChunks;
+                        st_shared_zero16(at + (o / (L::kHalves * 8)) * L::kKvTile + (o / 8 % L::kHalves) * L::kKvRegion +
+                                         r * 128 + (o % 8) * 16);
+                    }
+                    fence_proxy_async();                            // ahead of the products, and of the stage's next load
+                    __syncwarp(wmask);
+                } else {
+                    if (leader) mbar_expect_tx(&full[s], L::kTileBytes);
+                    __syncwarp(wmask);
+                    if (lane < 2 * L::kHalves)
+                        tma_load_3d(st + tv * L::kKvTile + hf * L::kKvRegion, tv ? &tm_v : &tm_k, &full[s], hf * 64,
+                                    sg.hk, row, pol);
                 }
             }
             // in run-time claims the second tile may precede the first
