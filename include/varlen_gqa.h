@@ -60,7 +60,8 @@ extern "C" {
 
 /* Sticky device-side error bits, read by attn_check_error().  When a
  * sequence trips one, none of its output rows are written. */
-#define ATTN_DEV_ERR_OFFSETS 0x1u      /* cu_q / cu_k negative or decreasing  */
+#define ATTN_DEV_ERR_OFFSETS 0x1u      /* cu_q / cu_k negative, decreasing, or
+                                          past the rows that a call states    */
 #define ATTN_DEV_ERR_Q_TOO_LONG 0x2u   /* Lq_b > max_q of the plan            */
 #define ATTN_DEV_ERR_K_TOO_LONG 0x4u   /* Lk_b > s_max of the plan            */
 #define ATTN_DEV_ERR_TIMEOUT 0x8u      /* a bounded pipeline wait gave up      */
@@ -233,6 +234,26 @@ int attn_run_strided(attn_plan_t plan, const void *q, const void *k, const void 
                      int64_t k_token_stride, int64_t v_token_stride, void *stream);
 
 /*
+ * attn_run_rows -- attn_run_strided with the buffers' rows stated: the form to
+ * prefer.
+ *
+ *   T_q, T_kv  rows of q, out and lse, and of k and v, in [0, 2^31): at least
+ *          cu_q[B_max] and cu_k[B_max].  No address outside them is asked for
+ *          or prefetched; a sequence whose offsets reach past them sets
+ *          ATTN_DEV_ERR_OFFSETS and is left unwritten.  With T_q = 0 the call
+ *          does nothing (q, out and lse may be NULL), with T_kv = 0 k and v
+ *          may be NULL.
+ *
+ * Without them (attn_run, attn_run_strided) the kernels hold no bound of the
+ * buffers: loads stay within the rows that cu_seqlens name and the zero fill
+ * before a tensor's first row, and what is prefetched while the work before the
+ * call may still change the lengths stays within k's and v's allocations.
+ */
+int attn_run_rows(attn_plan_t plan, const void *q, int64_t T_q, const void *k, const void *v, int64_t T_kv,
+                  int64_t k_token_stride, int64_t v_token_stride, const int32_t *cu_q, const int32_t *cu_k,
+                  void *out, float *lse, void *stream);
+
+/*
  * attn_run_paged -- attn_run over a paged K/V cache.
  *
  *   k_cache, v_cache  device, bf16, 16-byte aligned: num_pages pages of
@@ -272,6 +293,12 @@ int attn_run_paged(attn_plan_t plan, const void *q, const void *k_cache, const v
                    int64_t page_stride, int64_t token_stride, int page_size, int num_pages,
                    const int32_t *block_table, int bt_stride, const int32_t *cu_q,
                    const int32_t *cu_k, void *out, float *lse, void *stream);
+
+/* attn_run_paged with T_q, the rows of q, out and lse, as in attn_run_rows. */
+int attn_run_paged_rows(attn_plan_t plan, const void *q, int64_t T_q, const void *k_cache, const void *v_cache,
+                        int64_t page_stride, int64_t token_stride, int page_size, int num_pages,
+                        const int32_t *block_table, int bt_stride, const int32_t *cu_q, const int32_t *cu_k,
+                        void *out, float *lse, void *stream);
 
 /*
  * attn_merge_lse -- combine n attention results computed over disjoint key
@@ -452,7 +479,8 @@ int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int64_t x_token_
  *            (multiples of 8, at least a token's heads), so the parts of one
  *            fused projection work.  q and q_out may both be NULL: only the
  *            cache is written
- *   T_q      rows of q, k, v and pos, >= cu_q[B_max]
+ *   T_q      rows of q, k, v and pos, >= cu_q[B_max] (a sequence past them is
+ *            an error of its offsets)
  *   q_out    device, bf16 [T_q, Hq, D] packed, 16-byte aligned: the rotated
  *            queries, ready for attn_run_paged.  q itself where q is packed,
  *            or apart from q, k and v
@@ -480,7 +508,7 @@ int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void *q, int64_t
  *   q, k, cu_q, cu_k  as in attn_run_strided (the same tensors, after
  *            rotation); k_token_stride as there
  *   T_q, T_kv  rows of q and lse, and of k: at least cu_q[B_max] and
- *            cu_k[B_max].  No row of q or k past them is read
+ *            cu_k[B_max], as in attn_run_rows
  *   lse      device, fp32 [T_q, Hq]: the call's attn_run* result
  *   weight_in, weight_out  device, fp32 ledgers of leading dimension ld; in may
  *            be NULL (nothing gathered yet), or out itself, or apart from it

@@ -33,7 +33,7 @@ ATTN_DTYPE_BF16, ATTN_DTYPE_F16, ATTN_DTYPE_F32 = 0, 1, 2
 ATTN_ROPE_HALF, ATTN_ROPE_INTERLEAVED = 0, 1
 
 EXPORTED = ("attn_plan", "attn_plan_ex", "attn_plan_info", "attn_run", "attn_run_strided", "attn_run_paged",
-            "attn_merge_lse", "attn_check_error", "attn_destroy", "attn_strerror", "attn_rope_create",
+            "attn_run_rows", "attn_run_paged_rows", "attn_merge_lse", "attn_check_error", "attn_destroy", "attn_strerror", "attn_rope_create",
             "attn_rope_destroy", "attn_rope_apply", "attn_append_paged", "attn_key_weights", "attn_key_weights_paged",
             "attn_evict_paged")
 
@@ -91,6 +91,10 @@ def lib() -> ctypes.CDLL:
         i64 = ctypes.c_int64
         L.attn_run_paged.argtypes = [vp, vp, vp, vp, i64, i64, i, i, i32p, i, i32p, i32p, vp, vp, vp]
         L.attn_run_paged.restype = i
+        L.attn_run_rows.argtypes = [vp, vp, i64, vp, vp, i64, i64, i64, i32p, i32p, vp, vp, vp]
+        L.attn_run_rows.restype = i
+        L.attn_run_paged_rows.argtypes = [vp, vp, i64, vp, vp, i64, i64, i, i, i32p, i, i32p, i32p, vp, vp, vp]
+        L.attn_run_paged_rows.restype = i
         L.attn_merge_lse.argtypes = [i, vp, vp, i64, i32p, i, i, i, vp, vp, vp]
         L.attn_merge_lse.restype = i
         L.attn_check_error.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
@@ -311,7 +315,7 @@ class Plan:
         q [T_q, Hq, D] bf16 contiguous CUDA tensor; k / v [T_kv, Hkv, D] bf16
         CUDA tensors whose heads are contiguous within a token -- packed, or
         views into a larger buffer with a token stride (e.g. the halves of a
-        fused [T, 2, Hkv, D] cache), which go through attn_run_strided;
+        fused [T, 2, Hkv, D] cache).  Goes through attn_run_rows;
         cu_q / cu_k int32 CUDA tensors with B_max + 1 entries; out / lse are
         allocated when not given (pass them for graph capture)."""
         out, lse = self._check_common(q, cu_q, cu_k, out, lse, "attn_run", stream)
@@ -326,15 +330,10 @@ class Plan:
         packed = i["Hkv"] * i["D"]
         ks = k.stride(0) if k.shape[0] > 1 else packed
         vs = v.stride(0) if v.shape[0] > 1 else packed
-        if ks == packed and vs == packed:
-            rc = lib().attn_run(self._h, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
-                                cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(), _stream_ptr(stream))
-            _check(rc, "attn_run")
-        else:
-            rc = lib().attn_run_strided(self._h, q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_q.data_ptr(),
-                                        cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(), ks, vs,
-                                        _stream_ptr(stream))
-            _check(rc, "attn_run_strided")
+        rc = lib().attn_run_rows(self._h, q.data_ptr(), q.shape[0], k.data_ptr(), v.data_ptr(),
+                                 min(k.shape[0], v.shape[0]), ks, vs, cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), _stream_ptr(stream))
+        _check(rc, "attn_run")
         return out, lse
 
     def run_paged(self, q, k_cache, v_cache, block_table, cu_q, cu_k, out=None, lse=None, stream=None):
@@ -346,7 +345,7 @@ class Plan:
         block_table [B_max, n] int32 CUDA tensor, row b listing the pages of
         sequence b in key order (n >= ceil(s_max / page_size), row stride
         free); cu_k supplies the key lengths only.  Goes through
-        attn_run_paged."""
+        attn_run_paged_rows."""
         out, lse = self._check_common(q, cu_q, cu_k, out, lse, "attn_run_paged", stream)
         i = self.info
         shape = None
@@ -368,10 +367,10 @@ class Plan:
             raise ValueError("block_table must be an int32 CUDA tensor [B_max, n] with unit column stride")
         if bt.shape[1] * page_size < i["s_max"]:
             raise ValueError("block_table rows must cover s_max keys")
-        rc = lib().attn_run_paged(self._h, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), int(pstride),
-                                  int(tok), page_size, n_pages, bt.data_ptr(), int(bt.stride(0)),
-                                  cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                  _stream_ptr(stream))
+        rc = lib().attn_run_paged_rows(self._h, q.data_ptr(), q.shape[0], k_cache.data_ptr(), v_cache.data_ptr(),
+                                       int(pstride), int(tok), page_size, n_pages, bt.data_ptr(), int(bt.stride(0)),
+                                       cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                       _stream_ptr(stream))
         _check(rc, "attn_run_paged")
         return out, lse
 

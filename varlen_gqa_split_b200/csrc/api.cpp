@@ -25,6 +25,17 @@ namespace {
 std::mutex g_mu;
 std::unordered_set<attn_plan_s *> g_plans;
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+PFN_cuMemGetAddressRange_v3020 g_range = nullptr;
+
+// rows of `stride` elements from `base` that lie in the allocation it belongs
+// to, as far as it is known (0 otherwise)
+long long mapped_rows(const void *base, long long stride) {
+    CUdeviceptr start = 0;
+    size_t bytes = 0;
+    const CUdeviceptr at = reinterpret_cast<CUdeviceptr>(base);
+    if (!g_range || g_range(&start, &bytes, at) != CUDA_SUCCESS || at < start || at >= start + bytes) return 0;
+    return (long long)((start + bytes - at) / (size_t)(stride * 2));
+}
 
 }  // namespace
 
@@ -44,15 +55,19 @@ int get_encoder() {
         q != cudaDriverEntryPointSuccess || !fn)
         return ATTN_E_CUDA;
     g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    if (cudaGetDriverEntryPoint("cuMemGetAddressRange", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+        g_range = reinterpret_cast<PFN_cuMemGetAddressRange_v3020>(fn);
     return ATTN_OK;
 }
 
 // [T, Hkv, D] bf16, box = 64 elements x 1 head x block_n tokens, 128-byte
-// swizzle.  Packed K/V leave the token extent open (2^31 - 1): every load the
-// kernel issues ends at or before its sequence's last key (cu_k[b+1] - 1), so
-// the real buffer length never enters.  A paged cache passes its row count,
-// so a load at row num_pages * page_rows (the kernels' stand-in for a key
-// past the sequence or a bad table entry) lies outside and fills zeros.
+// swizzle.  Packed K/V end with the buffer's rows; where the caller did not
+// state them the extent is open (2^31 - 1), and every load the kernel issues
+// ends at or before its sequence's last key (cu_k[b+1] - 1).  A paged cache
+// passes its row count, so a load at row num_pages * page_rows (the kernels'
+// stand-in for a key past the sequence or a bad table entry) lies outside and
+// fills zeros.
 int encode_kv_map(CUtensorMap *map, const void *base, int Hkv, int D, int block_n, long long token_stride,
                   long long rows) {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)rows};
@@ -125,7 +140,7 @@ namespace vgqa {
 
 // [T, Hq, D] bf16, box = 64 elements x G heads x qtile tokens: one unit's
 // query rows (token-major, heads inner) as the tcgen05 kernel's A operand.
-// Loads are right-aligned to the sequence's last query token, so, as for K/V,
+// Loads are right-aligned to the row tile's last query token, so, as for K/V,
 // the token extent may be left open.
 int encode_q_map(CUtensorMap *map, const void *base, int Hq, int D, int G, int qtile, long long rows) {
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hq, (cuuint64_t)rows};
@@ -485,9 +500,14 @@ namespace {
 
 int run_impl(attn_plan_t plan, const void *q, const void *k, const void *v, const int32_t *cu_q,
              const int32_t *cu_k, void *out, float *lse, long long k_stride, long long v_stride,
-             const Paging *pg, void *stream) {
+             const Paging *pg, void *stream, int64_t T_q = kRowsOpen, int64_t T_kv = kRowsOpen) {
     if (!plan || !live(plan)) return ATTN_E_BAD_PLAN;
-    if (!q || !k || !v || !cu_q || !cu_k || !out || !lse) return ATTN_E_NULL;
+    if (T_q < 0 || T_q > kRowsOpen || T_kv < 0 || T_kv > kRowsOpen) return ATTN_E_INVALID_ARG;
+    if (!cu_q || !cu_k) return ATTN_E_NULL;
+    if (T_q == 0) return ATTN_OK;                     // no row to write (and tensors without rows have no address)
+    if (T_kv == 0 && !k) k = plan->scratch;           // never read: every sequence is empty
+    if (T_kv == 0 && !v) v = plan->scratch;
+    if (!q || !k || !v || !out || !lse) return ATTN_E_NULL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(cu_q, 4) || !aligned(cu_k, 4))
         return ATTN_E_ALIGNMENT;
@@ -509,6 +529,13 @@ int run_impl(attn_plan_t plan, const void *q, const void *k, const void *v, cons
     p.err = plan->err;
     p.stall = plan->err + 1;
     p.wait_ns = plan->wait_ns;
+    p.rows_q = (int)T_q;
+    p.rows_kv = pg ? kRowsOpen : (int)T_kv;
+    const long long rows_q = T_q, rows_kv = T_kv > 0 ? T_kv : 1;     // of the tensor maps
+    if (!pg && d.variant != ATTN_VARIANT_SIMT)
+        p.spec_rows = (int)(T_kv < kRowsOpen ? T_kv
+                                             : std::min<long long>(std::min(mapped_rows(k, k_stride), mapped_rows(v, v_stride)),
+                                                                   kRowsOpen));
     p.B_max = d.B_max;
     p.s_max = d.s_max;
     p.Hq = d.Hq;
@@ -566,8 +593,8 @@ int run_impl(attn_plan_t plan, const void *q, const void *k, const void *v, cons
                                     pg->page_stride) == ATTN_OK &&
                    encode_paged_map(&tm_v, v, d.Hkv, d.D, pg->page_size, pg->num_pages, v_stride,
                                     pg->page_stride) == ATTN_OK;
-        return encode_kv_map(&tm_k, k, d.Hkv, d.D, d.block_n, k_stride) == ATTN_OK &&
-               encode_kv_map(&tm_v, v, d.Hkv, d.D, d.block_n, v_stride) == ATTN_OK;
+        return encode_kv_map(&tm_k, k, d.Hkv, d.D, d.block_n, k_stride, rows_kv) == ATTN_OK &&
+               encode_kv_map(&tm_v, v, d.Hkv, d.D, d.block_n, v_stride, rows_kv) == ATTN_OK;
     };
     cudaError_t e;
     if (d.variant == ATTN_VARIANT_MMA) {
@@ -579,7 +606,7 @@ int run_impl(attn_plan_t plan, const void *q, const void *k, const void *v, cons
                  encode_paged_map_halves(&tm_v, v, d.Hkv, d.D, pg->page_size, pg->num_pages, v_stride,
                                          pg->page_stride) == ATTN_OK;
         else {
-            const long long rows = pg ? (long long)pg->num_pages * p.page_rows : 0x7fffffffll;
+            const long long rows = pg ? (long long)pg->num_pages * p.page_rows : rows_kv;
             const int box = pg ? std::min(pg->page_size, 64) : d.block_n;
             ok = encode_kv_map_halves(&tm_k, k, d.Hkv, d.D, box, k_stride, rows) == ATTN_OK &&
                  encode_kv_map_halves(&tm_v, v, d.Hkv, d.D, box, v_stride, rows) == ATTN_OK;
@@ -588,7 +615,7 @@ int run_impl(attn_plan_t plan, const void *q, const void *k, const void *v, cons
         e = launch_split_mma(p, tm_k, tm_v, plan->NT, d.stages, d.ctas, s);
     } else if (d.variant == ATTN_VARIANT_TC) {
         CUtensorMap tm_q, tm_k, tm_v;
-        if (encode_q_map(&tm_q, q, d.Hq, d.D, d.G, plan->qtile) != ATTN_OK || !kv_maps(tm_k, tm_v))
+        if (encode_q_map(&tm_q, q, d.Hq, d.D, d.G, plan->qtile, rows_q) != ATTN_OK || !kv_maps(tm_k, tm_v))
             return ATTN_E_CUDA;
         e = launch_split_tc(p, tm_q, tm_k, tm_v, d.stages, d.ctas, s);
     } else {
@@ -614,24 +641,38 @@ ATTN_EXPORT int attn_run(attn_plan_t plan, const void *q, const void *k, const v
 ATTN_EXPORT int attn_run_strided(attn_plan_t plan, const void *q, const void *k, const void *v,
                                  const int32_t *cu_q, const int32_t *cu_k, void *out, float *lse,
                                  int64_t k_token_stride, int64_t v_token_stride, void *stream) {
+    return attn_run_rows(plan, q, kRowsOpen, k, v, kRowsOpen, k_token_stride, v_token_stride, cu_q, cu_k, out, lse, stream);
+}
+
+ATTN_EXPORT int attn_run_rows(attn_plan_t plan, const void *q, int64_t T_q, const void *k, const void *v, int64_t T_kv,
+                              int64_t k_token_stride, int64_t v_token_stride, const int32_t *cu_q, const int32_t *cu_k,
+                              void *out, float *lse, void *stream) {
     if (!plan || !live(plan)) return ATTN_E_BAD_PLAN;
     const long long packed = (long long)plan->d.Hkv * plan->d.D;
     // a token's heads stay contiguous; the token stride keeps 16-byte
     // alignment (the tensor-map rule) and fits the tensor map's range
     for (long long st : {(long long)k_token_stride, (long long)v_token_stride})
         if (st < packed || st % 8 != 0 || st > (1ll << 38)) return ATTN_E_INVALID_ARG;
-    return run_impl(plan, q, k, v, cu_q, cu_k, out, lse, k_token_stride, v_token_stride, nullptr, stream);
+    return run_impl(plan, q, k, v, cu_q, cu_k, out, lse, k_token_stride, v_token_stride, nullptr, stream, T_q, T_kv);
 }
 
 ATTN_EXPORT int attn_run_paged(attn_plan_t plan, const void *q, const void *k_cache, const void *v_cache,
                                int64_t page_stride, int64_t token_stride, int page_size, int num_pages,
                                const int32_t *block_table, int bt_stride, const int32_t *cu_q,
                                const int32_t *cu_k, void *out, float *lse, void *stream) {
+    return attn_run_paged_rows(plan, q, kRowsOpen, k_cache, v_cache, page_stride, token_stride, page_size, num_pages,
+                               block_table, bt_stride, cu_q, cu_k, out, lse, stream);
+}
+
+ATTN_EXPORT int attn_run_paged_rows(attn_plan_t plan, const void *q, int64_t T_q, const void *k_cache,
+                                    const void *v_cache, int64_t page_stride, int64_t token_stride, int page_size,
+                                    int num_pages, const int32_t *block_table, int bt_stride, const int32_t *cu_q,
+                                    const int32_t *cu_k, void *out, float *lse, void *stream) {
     if (!plan || !live(plan)) return ATTN_E_BAD_PLAN;
     const int rc = check_paging(plan, page_stride, token_stride, page_size, num_pages, block_table, bt_stride);
     if (rc != ATTN_OK) return rc;
     const Paging pg{block_table, bt_stride, page_size, num_pages, page_stride};
-    return run_impl(plan, q, k_cache, v_cache, cu_q, cu_k, out, lse, token_stride, token_stride, &pg, stream);
+    return run_impl(plan, q, k_cache, v_cache, cu_q, cu_k, out, lse, token_stride, token_stride, &pg, stream, T_q);
 }
 
 ATTN_EXPORT int attn_check_error(attn_plan_t plan, void *stream, uint32_t *flags) {

@@ -42,6 +42,8 @@ int key_weights(attn_plan_t plan, const void *q, long long T_q, const void *k, l
     p.lse = const_cast<float *>(lse);
     p.err = plan->err;
     p.wait_ns = plan->wait_ns;
+    p.rows_q = (int)T_q;
+    if (!pg) p.rows_kv = (int)T_kv;
     p.B_max = d.B_max;
     p.s_max = d.s_max;
     p.Hq = d.Hq;
@@ -65,10 +67,7 @@ int key_weights(attn_plan_t plan, const void *q, long long T_q, const void *k, l
 
     p.qtile = plan->kw_qtile;
     CUtensorMap tm_q, tm_k;
-    // The maps end where the buffers end.  With an open extent a box that began
-    // before the first row of a short K (67 rows, 29 KB before the end of their
-    // mapping) touched addresses past it: an extent must not claim what is not
-    // there.
+    // the maps end where the buffers end, and no box starts before their first row
     int rc = encode_q_map(&tm_q, q, d.Hq, d.D, d.G, p.qtile, T_q > 0 ? T_q : 1);
     if (rc != ATTN_OK) return rc;
     if (pg) {

@@ -221,6 +221,10 @@ struct Walker {
         const int j = kt * kItemKeys + u * kSubKeys;
         return j < s.Lk ? j : -1;
     }
+    // first token of row tile r's box of queries: the box ends with the tile, or
+    // starts with the buffer; and the tokens from there to the tile's end
+    __device__ int first_token(int r, int qtile) const { return max(s.Lq - (r + 1) * qtile, -s.q0); }
+    __device__ int tokens(int r, int qtile) const { return s.Lq - r * qtile - first_token(r, qtile); }
     // where the box of packed K starts, in keys from the sequence's first (maybe
     // before it): moved back to end with the sequence, but not before row 0
     __device__ int packed_start(int j0) const { return max(min(j0, s.Lk - kSubKeys), -s.k0); }
@@ -372,10 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 if (nq >= QS && !(ok = wait_all(&q_empty[qs], qph ^ 1))) break;
                 if (lane == 0) mbar_arrive_expect_tx(&q_full[qs], q_bytes);
                 __syncwarp();
-                // the box ends with the row tile's last token
                 if (lane < L::kHalves)
                     tma_load_3d(ring_q + qs * L::kQ + lane * (N * 128), &tm_q, &q_full[qs], lane * 64, it.hk * G,
-                                it.s.q0 + it.s.Lq - (r + 1) * QT, pol_q);
+                                it.s.q0 + it.first_token(r, QT), pol_q);
                 ++nq;
                 if (++qs == QS) {
                     qs = 0;
@@ -494,13 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
         do {
             if (it.R == 0) continue;
             for (int r = it.r0; r < it.r1 && ok; ++r, ++j) {
-                const int t0 = it.s.Lq - (r + 1) * QT;                     // may be negative: those rows do not exist
+                const int t0 = it.first_token(r, QT);                      // may be negative: another sequence's rows
+                const int lo = max(0, it.s.Lq - (r + 1) * QT), hi = it.s.Lq - r * QT;   // the tile's tokens
                 const float *src = p.lse + ((long long)it.s.q0 + t0) * p.Hq + it.hk * G;
                 float v[kPer];
                 bool skip = false;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) {
-                    const bool row = tok[i] >= 0 && t0 + tok[i] >= 0;
+                    const bool row = tok[i] >= 0 && t0 + tok[i] >= lo && t0 + tok[i] < hi;
                     v[i] = row ? src[off[i]] : -INFINITY;
                     skip |= row && v[i] == -INFINITY;
                 }
@@ -553,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 const int buf = j & 1;
                 if (!__all_sync(0xffffffffu, ready) && !(ok = wwait(&s_full[buf], (j >> 1) & 1))) break;
                 tc::fence_after_sync();
-                const int t0 = it.s.Lq - (it.r0 + i + 1) * QT;
+                const int t0 = it.first_token(it.r0 + i, QT);
+                const int cols = min(ncols, it.tokens(it.r0 + i, QT) * G);   // columns of the tile's tokens
                 const bool skip = skips[buf] != 0;
                 // every column from `all_from` on sees all of the sub-tile's keys, none
                 // before `any_from` sees any of them
@@ -565,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
 #pragma unroll
                 for (int ch = 0; ch < kCols / 16; ++ch) {
                     const int c0 = col0 + ch * 16;
-                    const bool some = live && c0 + 16 > any_from && c0 < ncols;
+                    const bool some = live && c0 + 16 > any_from && c0 < cols;
                     uint32_t v[16];
                     if (some) {
                         tc::ld_32x32b_x16(tb + ch * 16, v);
@@ -580,12 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                         ready = mbar_test_wait(&s_full[buf ^ 1], ((j + 1) >> 1) & 1);
                     }
                     if (some) {
-                        if (c0 >= all_from && c0 + 16 <= ncols && !skip) {
+                        if (c0 >= all_from && c0 + 16 <= cols && !skip) {
                             add_columns<false>(v, n0 + ch * 16, scale, 0, acc);
                         } else {
-                            // columns [first, ncols) see this key
+                            // columns [first, cols) see this key
                             const int first = max(0, max(-t0, key - old - t0)) * G;
-                            const int lo = min(16, max(0, first - c0)), hi = min(16, ncols - c0);
+                            const int lo = min(16, max(0, first - c0)), hi = min(16, cols - c0);
                             add_columns<true>(v, n0 + ch * 16, scale, (1u << hi) - (1u << min(lo, hi)), acc);
                         }
                     }

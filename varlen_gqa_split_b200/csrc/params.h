@@ -10,6 +10,9 @@ namespace vgqa {
 // Default upper bound on one bounded wait, in nanoseconds of %globaltimer.
 constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
 
+// Row counts that the caller did not state (Params::rows_q, rows_kv).
+constexpr int kRowsOpen = 0x7fffffff;
+
 // Everything a split / combine launch needs.  Passed by value.
 struct Params {
     const __nv_bfloat16 *q;    // [T_q, Hq, D]
@@ -26,6 +29,9 @@ struct Params {
     unsigned long long *claim; // [B_max * Hkv] tile claims of cut units (tensor-core path)
     uint32_t *done;            // [B_max * Hkv] parts written / merges started per cut unit
     int B_max, s_max, Hq, Hkv, D, max_q, G;
+    int rows_q = kRowsOpen;    // rows of q (out, lse), and of packed k and v: offsets past them are errors,
+    int rows_kv = kRowsOpen;   // and no box of a tensor starts before its first row
+    int spec_rows;             // rows of packed k and v that may be prefetched whatever the lengths read
     int nsplit;                // chunks per (sequence, KV head)
     int chunk;                 // keys per chunk
     int rows_per_block;        // query rows (G * tokens) per block

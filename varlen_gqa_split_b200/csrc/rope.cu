@@ -420,6 +420,7 @@ ATTN_EXPORT int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void
     p.Hkv = d.Hkv;
     p.D = d.D;
     p.max_q = d.max_q;
+    p.rows_q = (int)T_q;
     p.k_stride = token_stride;
     p.block_table = block_table;
     p.bt_stride = bt_stride;

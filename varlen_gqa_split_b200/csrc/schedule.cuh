@@ -80,6 +80,15 @@ struct Segment {
     long long Pu;         // global index of the unit's first position
 };
 
+// Where the box of a packed sequence's last tile starts, in keys from its
+// first: it ends with the sequence.  Negative for a sequence of less than a
+// tile: the box starts in the one before it, but, where the buffer's rows are
+// stated, not before the buffer (it then ends in the one after it).  Every
+// tile t starts at min(t * kBN, this).
+__device__ __forceinline__ int last_start(const Params &p, int Lk, int k0) {
+    return p.rows_kv == kRowsOpen ? Lk - kBN : max(Lk - kBN, -k0);
+}
+
 // counters of unit (b, hk, rt): tile claims, part counts
 __device__ __forceinline__ long long unit_index(const Params &p, int b, int hk, int rt) {
     return ((long long)b * p.Hkv + hk) * p.max_rt + rt;

@@ -17,8 +17,9 @@
 // unit's loads are in flight while the current unit finishes.  A tile whose
 // keys would run past its sequence is loaded ending at the sequence's last
 // key (its start moves back, the extra keys are masked), so no load reads
-// past cu_k[b+1]; a start before the buffer is a negative TMA coordinate,
-// which the hardware fills with zeros.
+// past cu_k[b+1].  Where the buffer's rows are stated its tensor maps end
+// with them and no box starts before the first; where they are not, such a
+// start is a negative TMA coordinate, which the hardware fills with zeros.
 //
 // Consumers: warp w takes keys 16w .. 16w+15 of every tile and keeps its own
 // online-softmax state.  With at most 16 query rows the contraction keeps the
@@ -108,13 +109,14 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
     // L1) and, if its share starts on a unit shared with other blocks,
     // prefetches its first tiles into L2 (schedule.cuh first_tiles).  Both
     // are hints: the L2 is coherent, so a prefetched line never hides a later
-    // write, and the tensor map bounds every prefetch whatever the lengths
-    // read.
+    // write.  The lengths may still change and may read as anything, so only
+    // rows that are known to be there are prefetched.
     if constexpr (!PAGED && !DIRECT) {         // (direct mode: every share is a whole unit, nothing to prefetch)
         Share sp;
         if (block_share(p, c, gridDim.x, tid, kThreads, false, scan, first, sp, true) && warp == kConsumerWarps)
             first_tiles(p, c, sp, kPrefetchBytes / L::kStageBytes, true, [&](const Segment &sg, int t) {
                 const int row = sg.s.k0 + min(t * kBN, sg.s.Lk - kBN);
+                if (row < 0 || row > p.spec_rows - kBN) return;
                 tma_prefetch_4d(&tm_k, 0, sg.hk, row, 0);
                 tma_prefetch_4d(&tm_v, 0, sg.hk, row, 0);
             });
@@ -176,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
                 __syncwarp(wmask);
                 return ring + s * L::kStageBytes;
             };
-            auto load_tile = [&](const Segment &sg, int tile, bool last) -> bool {
+            int last = 0;                    // where the unit's last tile starts (packed)
+            auto load_tile = [&](const Segment &sg, int tile, bool end) -> bool {
                 const int ks = tile * kBN;
                 if constexpr (PAGED) {
                     // boxes of page_box keys, each from its page: lane i loads
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
                     const bool in = mine && key < sg.s.Lk;
                     const int entry = in ? page_entry(p, sg.b, key) : 0;
                     if (!acquire()) return false;
-                    uint8_t *st = open_stage(ks, last);
+                    uint8_t *st = open_stage(ks, end);
                     if (mine) {
                         // a box past the sequence (or a bad entry) reads page
                         // num_pages, outside the map: zeros
@@ -207,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
                     return true;
                 }
                 if (!acquire()) return false;
-                const int row = sg.s.k0 + min(ks, sg.s.Lk - kBN);
-                uint8_t *st = open_stage(ks, last);
+                const int row = sg.s.k0 + min(ks, last);
+                uint8_t *st = open_stage(ks, end);
                 // one box per tensor fills the tile's halves ([half][row][128 B])
                 if (lane < 2)
                     tma_load_4d(st + lane * L::kTileBytes, lane ? &tm_v : &tm_k, &full[s], 0, sg.hk, row, 0, pol);
@@ -226,6 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
             };
             auto begin = [&](const Segment &sg, int) -> bool {
                 if constexpr (PAGED) prefetch_pages(p, sg.b, sg.s.Lk, lane, 32);
+                if constexpr (!PAGED) last = last_start(p, sg.s.Lk, sg.s.k0);
                 return true;
             };
             feed_tiles<true>(p, b_first, pb_first, lo, hi, begin, load_tile, empty_stage);
@@ -309,15 +313,15 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
 
-        // The box of a packed sequence of less than a tile starts before it, on
-        // rows of another one.  This warp zeroes its rows of them in V: their
-        // weights are 0, but 0 times a non-finite value would not be (rows
-        // before the buffer's first came as zeros).  The unit has this one
-        // tile.  (256 sequences of 40 keys, 8 KV heads: 36.5 -> 38.5 us a call;
+        // The box of a packed sequence of less than a tile holds rows of others.
+        // This warp zeroes its rows of them in V: their weights are 0, but 0
+        // times a non-finite value would not be (rows outside the buffer came
+        // as zeros).  The unit has this one tile.  (256 sequences of 40 keys, 8 KV heads: 36.5 -> 38.5 us a call;
         // inside the loop it would cost every batch 1 to 2%, and a producer
         // that waits for such a tile and zeroes costs 2% of a ragged batch with
         // two such sequences.)
-        if (!PAGED && Lk < kBN && cur.s.k0 > 0 && mbar_wait(&full[s], phase, p.wait_ns) &&
+        const int last = last_start(p, Lk, cur.s.k0);
+        if (!PAGED && Lk < kBN && (cur.s.k0 > 0 || p.rows_kv != kRowsOpen) && mbar_wait(&full[s], phase, p.wait_ns) &&
             !(meta[s].y & kMetaEmpty)) {
             constexpr int kChunks = L::kHalves * 8, kStep = 32 / kChunks;     // 16-byte pieces of a row, rows at once
             const int r0 = kbase + lane / kChunks, piece = lane % kChunks;
@@ -325,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
                                 (piece & 7) * 16;
 #pragma unroll
             for (int i = 0; i < 16; i += kStep)
-                if (r0 + i < kBN - Lk && r0 + i >= kBN - Lk - cur.s.k0) st_shared_zero16(at + i * 128);
+                if ((unsigned)(last + r0 + i) >= (unsigned)Lk) st_shared_zero16(at + i * 128);
             fence_proxy_async();                    // ahead of the stage's next load
             __syncwarp();
         }
@@ -352,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
             // was moved back to end at its last key; a paged tile starts at
             // t0, and its rows past Lk hold whatever the page held
             constexpr bool paged = PAGED;
-            const int ls = paged ? t0 : min(t0, Lk - kBN);
+            const int ls = paged ? t0 : min(t0, last);
             bool zeroed = false;
             if (paged && t0 + kBN > Lk) {
                 // zero this warp's V rows past Lk: their weights are 0, but

@@ -111,9 +111,11 @@ struct TcLayout {
 // entry is rewritten only after the softmax warps have left its unit.
 struct UnitDesc {
     int b, hk, rt, role;                  // role 0: the unit is the block's alone; 1, 2: cut (OrderedWalker)
-    int q0, Lq, Lk, w;                    // w: the unit's positions in the flattened tile space
+    int Lk, last, w, nq;                  // last: where its last tile starts (last_start); w: its positions in the
+                                          // flattened tile space; nq: its query tokens
     long long Pu;                         // global index of its first position
-    long long pad;
+    int tok0, box, vis0, pad;             // its first query token's row of q; the box's first one, from there
+                                          // (<= 0); the keys its first token sees
 };
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -198,13 +200,14 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
     // previous kernel in the stream still runs.  Meanwhile it prefetches its
     // first K/V tiles into L2 under a speculative schedule (the warp-MMA
     // kernel does the same; both are hints that no later write can make
-    // stale).  Then it waits for that kernel before the reads that count;
+    // stale, and stay in rows that are known to be there).  Then it waits for that kernel before the reads that count;
     // only then may this call's combine kernel launch.
     if constexpr (!PAGED) {
         Share sp;
         if (block_share(p, c, gridDim.x, tid, kThreads, false, scan, first, sp, true) && warp == kProducerWarp)
             first_tiles<FUSED>(p, c, sp, kPrefetchBytes / (int)L::kTileBytes, true, [&](const Segment &sg, int t) {
                 const int row = sg.s.k0 + min(t * kBN, sg.s.Lk - kBN);
+                if (row < 0 || row > p.spec_rows - kBN) return;
 #pragma unroll
                 for (int hf = 0; hf < L::kHalves; ++hf) {
                     tma_prefetch_3d(&tm_k, hf * 64, sg.hk, row);
@@ -238,6 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
         uint32_t phase = 0;
         int nseg = 0;                        // units begun
         uint32_t lone_phase = 0;
+        int last_at = 0;                     // where the unit's last tile starts (packed)
+        bool alone = false;                  // ... and is its only one, with rows of other sequences
         int nsub = 0;                        // tiles in the open stage (0: none open)
         int ks_a = 0, ks_b = 0;              // key starts of the open stage's tiles
         auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -273,6 +278,10 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
                 mneed = (uint32_t)((c - block_of(sg.Pu, sh.T, sh.Ce)) * kSoftWarps) + *p.stall;
             }
             if constexpr (PAGED) prefetch_pages(p, sg.b, sg.s.Lk, lane, 32);
+            if constexpr (!PAGED) {
+                last_at = last_start(p, sg.s.Lk, sg.s.k0);
+                alone = sg.s.Lk < kBN && (sg.s.k0 > 0 || p.rows_kv != kRowsOpen);
+            }
             if (!acquire()) return false;
             if (leader) {
                 UnitDesc &u = units[nseg % kSegRing];
@@ -280,19 +289,24 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
                 u.hk = sg.hk;
                 u.rt = sg.rt;
                 u.role = role;
-                u.q0 = sg.s.q0;
-                u.Lq = sg.s.Lq;
+                // the box ends at the row tile's last query token, or starts
+                // with the buffer where its rows are stated
+                const int end = sg.s.Lq - sg.rt * QT, t0 = max(0, end - QT);
+                const int box = p.rows_q == kRowsOpen ? end - QT : max(end - QT, -sg.s.q0);
                 u.Lk = sg.s.Lk;
+                u.last = last_at;
                 u.w = sg.w;
+                u.nq = end - t0;
                 u.Pu = sg.Pu;
+                u.tok0 = sg.s.q0 + t0;
+                u.box = box - t0;
+                u.vis0 = sg.s.Lk - sg.s.Lq + t0 + 1;
                 meta[s] = make_int4(0, -1, kMetaQ, nseg);
                 mbar_arrive_expect_tx(&full[s], q_bytes);
-                // the box ends at the row tile's last query token
-                const int t_end = sg.s.q0 + sg.s.Lq - sg.rt * QT;
 #pragma unroll
                 for (int hf = 0; hf < L::kHalves; ++hf)
                     tma_load_3d(ring + s * L::kStage + hf * L::kQRegion, &tm_q, &full[s], hf * 64, sg.hk * G,
-                                t_end - QT, pol);
+                                sg.s.q0 + box, pol);
             }
             __syncwarp(wmask);
             advance();
@@ -332,17 +346,16 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
                 }
             } else {
                 if (nsub == 0 && !acquire()) return false;
-                // The box of a sequence of less than a tile starts before it, on
-                // rows of another one, whatever they hold: weight 0 times a
-                // non-finite value would not be 0.  The producer waits for such
-                // a tile (the only one of its unit) and zeroes those rows before
-                // the stage counts as full; softmax loops that did it took 2%
-                // longer on batches without such a sequence.  Rows before the
-                // buffer's first come as zeros.
-                const int row = sg.s.k0 + min(ks, sg.s.Lk - kBN);
+                // The box of a sequence of less than a tile holds rows of others,
+                // and whatever those hold: weight 0 times a non-finite value
+                // would not be 0.  The producer waits for such a tile (the only
+                // one of its unit) and zeroes those rows before the stage counts
+                // as full; softmax loops that did it took 2% longer on batches
+                // without such a sequence.  Rows outside the buffer come as zeros.
+                const int row = sg.s.k0 + min(ks, last_at);
                 uint8_t *st = ring + s * L::kStage + nsub * L::kSubRows;
                 const int tv = lane / L::kHalves, hf = lane % L::kHalves;   // lane: (K or V, D-half)
-                if (sg.s.Lk < kBN && sg.s.k0 > 0) {
+                if (alone) {
                     if (leader) mbar_arrive_expect_tx(lone, L::kTileBytes);
                     __syncwarp(wmask);
                     if (lane < 2 * L::kHalves)
@@ -354,14 +367,17 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
                     }
                     lone_phase ^= 1;
                     constexpr int kChunks = 2 * L::kHalves * 8;     // 16-byte pieces of a row of K and V
-                    const int from = max(0, kBN - sg.s.Lk - sg.s.k0), n = kBN - sg.s.Lk - from;
-                    const uint32_t at = smem_u32(st) + from * 128;
+                    const uint32_t at = smem_u32(st);
+                    auto zero_rows = [&](int from, int to) {
 #pragma unroll 1
-                    for (int i = lane; i < n * kChunks; i += 32) {
-                        const int r = i / kChunks, o = i % kChunks;
-                        st_shared_zero16(at + (o / (L::kHalves * 8)) * L::kKvTile + (o / 8 % L::kHalves) * L::kKvRegion +
-                                         r * 128 + (o % 8) * 16);
-                    }
+                        for (int i = lane; i < (to - from) * kChunks; i += 32) {
+                            const int r = from + i / kChunks, o = i % kChunks;
+                            st_shared_zero16(at + (o / (L::kHalves * 8)) * L::kKvTile +
+                                             (o / 8 % L::kHalves) * L::kKvRegion + r * 128 + (o % 8) * 16);
+                        }
+                    };
+                    zero_rows(max(0, -row), -last_at);
+                    zero_rows(sg.s.Lk - last_at, kBN);
                     fence_proxy_async();                            // ahead of the products, and of the stage's next load
                     __syncwarp(wmask);
                 } else {
@@ -642,12 +658,11 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
         ok = copy_q(more);
         while (ok && more) {
             const UnitDesc &u = units[(kq - 1) % kSegRing];      // the unit whose Q was copied last
-            const int Lq = u.Lq, Lk = u.Lk;
+            const int Lk = u.Lk, last = u.last;
             const int tq = r / G, g = r - tq * G;
-            const int box0 = Lq - (u.rt + 1) * QT;               // the row tile's first token (may be < 0)
-            const int qi = tq + box0;                            // this row's query token in the sequence
-            const bool valid = tq < QT && qi >= 0;
-            const int vis = valid ? Lk - Lq + qi + 1 : 0;        // keys [0, vis) visible (tail-aligned causal)
+            const int qr = tq + u.box;                           // this row's query token in the row tile
+            const bool valid = (unsigned)qr < (unsigned)u.nq;
+            const int vis = valid ? u.vis0 + qr : 0;             // keys [0, vis) visible (tail-aligned causal)
             // a lane quarter none of whose 32 rows is a query row of this
             // unit only keeps the barrier protocol (its P rows feed O rows
             // nobody reads); both warps of the quarter see the same rows
@@ -711,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
                 float mx = -INFINITY;
                 bool whole_rows = true, dead = false;            // dead: this row's weights are all 0
                 if (ks >= 0) {
-                    const int ls = PAGED ? ks : min(ks, Lk - kBN);      // key of column 0
+                    const int ls = PAGED ? ks : min(ks, last);          // key of column 0
                     // visible columns [lo_c, lo_c + width); a row past the unit's
                     // query rows sees none
                     const int lo_c = max(ks - ls, 0);
@@ -814,7 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
             // the next unit's Q goes to tensor memory now, so that its first
             // product can run during this unit's epilogue
             const int role = u.role, ub = u.b, uhk = u.hk, urt = u.rt, uw = u.w;
-            const long long uq0 = u.q0, uPu = u.Pu;
+            const int utok0 = u.tok0;
+            const long long uPu = u.Pu;
             if (!(ok = copy_q(more))) break;
 
             // ---------------- epilogue: this block's part of the unit
@@ -830,8 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
             }
             const bool whole = role == 0;
             const int slot = role == 1 ? 2 * c : 2 * c + 1;
-            const int pr = (qi - max(0, box0)) * G + g;         // row within the unit's partial
-            const long long tok = uq0 + qi;
+            const int pr = qr * G + g;                           // row within the unit's partial
+            const long long tok = utok0 + qr;
             const int h = uhk * G + g;
             const int d0 = half * L::kOCols;                     // this warp's first column of D
             const long long uidx = unit_index(p, ub, uhk, urt);
@@ -915,12 +931,11 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
             const UnitDesc &u = units[(kq - 1) % kSegRing];
             const long long m_uPu = u.Pu;
             const int tq = r / G, g = r - tq * G;
-            const int box0 = u.Lq - (u.rt + 1) * QT;
-            const int qi = tq + box0;
-            const bool m_valid = tq < QT && qi >= 0;
+            const int qr = tq + u.box;
+            const bool m_valid = (unsigned)qr < (unsigned)u.nq;
             const bool m_act = __any_sync(0xffffffffu, m_valid);
-            const int m_pr = (qi - max(0, box0)) * G + g;
-            const long long m_tok = u.q0 + qi;
+            const int m_pr = qr * G + g;
+            const long long m_tok = u.tok0 + qr;
             const int m_h = u.hk * G + g;
             const float2 st = mstash[tid];
             const float m_M = st.x, m_Lt = st.y;
