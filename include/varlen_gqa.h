@@ -508,7 +508,9 @@ int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void *q, int64_t
  *   q, k, cu_q, cu_k  as in attn_run_strided (the same tensors, after
  *            rotation); k_token_stride as there
  *   T_q, T_kv  rows of q and lse, and of k: at least cu_q[B_max] and
- *            cu_k[B_max], as in attn_run_rows
+ *            cu_k[B_max], as in attn_run_rows.  q and lse may be NULL with
+ *            T_q = 0 (the weights of earlier tokens are passed on, decayed),
+ *            k with T_kv = 0
  *   lse      device, fp32 [T_q, Hq]: the call's attn_run* result
  *   weight_in, weight_out  device, fp32 ledgers of leading dimension ld; in may
  *            be NULL (nothing gathered yet), or out itself, or apart from it

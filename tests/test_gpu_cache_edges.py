@@ -1,0 +1,79 @@
+"""Edges of the operators on the cache: calls without rows, infinite sums,
+strides that do not matter, overlapping outputs (needs a B200)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import varlen_gqa_split_b200 as vg
+import workloads as W
+from varlen_gqa_split_b200 import Plan, Rope, rope_table
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from varlen_gqa_split_b200 import build
+    build.build()
+    torch.cuda.init()
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _bf16(shape, seed):
+    return torch.randn(shape, generator=_gen(seed), device="cuda").to(torch.bfloat16)
+
+
+def _cu(lens):
+    return torch.from_numpy(W.cu_from_lengths(lens)).cuda()
+
+
+# ---------------------------------------------------------- calls without rows
+
+@pytest.mark.parametrize("Hq,Hkv,max_q", [(8, 2, 1), (4, 1, 300), (260, 2, 2)])
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("decay", [0.0, 0.5])
+def test_key_weights_without_queries(Hq, Hkv, max_q, paged, decay):
+    """No query in the whole batch: every key passes on its decayed weight."""
+    lk = np.array([300, 0, 17])
+    k = _bf16((317, Hkv, 64), 1)
+    plan = Plan(3, 300, Hq, Hkv, 64, max_q)
+    q, lse = torch.empty(0, Hq, 64, dtype=torch.bfloat16, device="cuda"), torch.empty(0, Hq, device="cuda")
+    w = torch.rand(3, Hkv, 300, generator=_gen(2), device="cuda")
+    out, born = torch.full_like(w, 7.0), torch.full((3, Hkv, 300), -5, dtype=torch.int32, device="cuda")
+    seen = torch.from_numpy(lk).int().cuda()
+    cu_q, cu_k = _cu([0, 0, 0]), _cu(lk)
+    kw = dict(decay=decay, out=out, seen=seen, born=born)
+    if paged:
+        pc = W.paginate(k, k, W.cu_from_lengths(lk), 3, 16, 300, seed=3)
+        plan.key_weights_paged(q, pc.k_cache, pc.block_table, cu_q, cu_k, lse, w, **kw)
+    else:
+        plan.key_weights(q, k, cu_q, cu_k, lse, w, **kw)
+    assert plan.check_error() == 0 and (born == -5).all()
+    for b, n in enumerate(lk):
+        assert torch.equal(out[b, :, :n], w[b, :, :n] * decay) and (out[b, :, n:] == 7.0).all()
+    # a batch that claims queries the tensor does not have
+    plan.key_weights(q, k, _cu([1, 0, 0]), cu_k, lse, w, out=out)
+    assert plan.check_error() == vg.ATTN_DEV_ERR_OFFSETS
+
+
+@pytest.mark.parametrize("Hq", [8, 260])
+def test_key_weights_without_keys(Hq):
+    plan = Plan(2, 64, Hq, 2, 64, 3)
+    k = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu = _cu([0, 0])
+    for T, lq in ((0, [0, 0]), (3, [3, 0])):
+        q, lse = _bf16((T, Hq, 64), 1), torch.full((T, Hq), -math.inf, device="cuda")
+        out = torch.full((2, 2, 64), 7.0, device="cuda")
+        plan.key_weights(q, k, _cu(lq), cu, lse, out=out)
+        assert plan.check_error() == 0 and (out == 7.0).all()
+        assert (plan.key_weights(q, k, _cu(lq), cu, lse) == 0).all()
+    # keys that the tensor does not have
+    plan.key_weights(_bf16((1, Hq, 64), 1), k, _cu([1, 0]), _cu([5, 0]), torch.zeros(1, Hq, device="cuda"), out=out)
+    assert plan.check_error() == vg.ATTN_DEV_ERR_OFFSETS and (out == 7.0).all()

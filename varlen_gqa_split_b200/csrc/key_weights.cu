@@ -12,6 +12,10 @@ namespace {
 int key_weights(attn_plan_t plan, const void *q, long long T_q, const void *k, long long k_stride, long long T_kv, const Paging *pg,
                 const int32_t *cu_q, const int32_t *cu_k, const float *lse, float decay, const float *weight_in,
                 float *weight_out, int64_t ld, const int32_t *seen, int32_t *born, void *stream) {
+    // tensors without rows have no address; none of these is read then
+    if (T_q == 0 && !q) q = plan->scratch;
+    if (T_q == 0 && !lse) lse = static_cast<const float *>(plan->scratch);
+    if (!pg && T_kv == 0 && !k) k = plan->scratch;
     if (!q || !k || !cu_q || !cu_k || !lse || !weight_out || !seen != !born) return ATTN_E_NULL;
     if (!aligned(q, 16) || !aligned(k, 16)) return ATTN_E_ALIGNMENT;
     for (const void *ptr : {(const void *)cu_q, (const void *)cu_k, (const void *)lse, (const void *)weight_in,
