@@ -77,3 +77,35 @@ def test_key_weights_without_keys(Hq):
     # keys that the tensor does not have
     plan.key_weights(_bf16((1, Hq, 64), 1), k, _cu([1, 0]), _cu([5, 0]), torch.zeros(1, Hq, device="cuda"), out=out)
     assert plan.check_error() == vg.ATTN_DEV_ERR_OFFSETS and (out == 7.0).all()
+
+
+# ---------------------------------------------------------------- infinities
+
+@pytest.mark.parametrize("Hq,Hkv,max_q", [(8, 2, 1), (8, 2, 40), (64, 64, 300), (136, 1, 40)])
+@pytest.mark.parametrize("paged", [False, True])
+def test_infinite_sums_stay_infinite(Hq, Hkv, max_q, paged):
+    """With normalisers far below the scores every weight that a visible row
+    gives is infinite, and so are the sums; what nothing adds to is finite."""
+    lk, lq = np.array([700, 300]), np.minimum(max_q, np.array([40, 300]))
+    plan = Plan(2, 700, Hq, Hkv, 64, max_q)
+    q, k = _bf16((int(lq.sum()), Hq, 64), 1), _bf16((1000, Hkv, 64), 2)
+    lse = torch.full((q.shape[0], Hq), -200.0, device="cuda")
+    w = torch.rand(2, Hkv, 700, generator=_gen(3), device="cuda")
+    w[0, 0, 5] = math.inf
+    cu_q, cu_k = _cu(lq), _cu(lk)
+    if paged:
+        pc = W.paginate(k, k, W.cu_from_lengths(lk), 2, 16, 700, seed=3)
+        out = plan.key_weights_paged(q, pc.k_cache, pc.block_table, cu_q, cu_k, lse, w)
+    else:
+        out = plan.key_weights(q, k, cu_q, cu_k, lse, w)
+    for b in range(2):
+        assert (out[b, :, :lk[b]] == math.inf).all(), b
+    lse[:] = math.inf                                            # and the other way: no row adds anything
+    if paged:
+        out = plan.key_weights_paged(q, pc.k_cache, pc.block_table, cu_q, cu_k, lse, w, out=out)
+    else:
+        out = plan.key_weights(q, k, cu_q, cu_k, lse, w, out=out)
+    for b in range(2):
+        old = int(lk[b] - lq[b])
+        assert torch.equal(out[b, :, :old], w[b, :, :old]) and (out[b, :, old:lk[b]] == 0).all()
+    assert plan.check_error() == 0

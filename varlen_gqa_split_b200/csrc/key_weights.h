@@ -19,4 +19,12 @@ struct KeyWeights {
     uint32_t *ticket;          // and counts of finished parts, eight per block (one a warp)
 };
 
+// total += part, compensated by `carry`: many thousand rows may add up.  An
+// infinite total is kept as it is (its compensation would be inf - inf).
+__device__ __forceinline__ void add_compensated(float &total, float &carry, float part) {
+    const float y = part - carry, t = total + y;
+    carry = fabsf(t) < INFINITY ? (t - total) - y : 0.f;
+    total = t;
+}
+
 }  // namespace vgqa

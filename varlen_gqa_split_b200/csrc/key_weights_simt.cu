@@ -88,10 +88,7 @@ __global__ void __launch_bounds__(kKeys) key_weights_simt_kernel(const Params p,
             }
             if (mine && r + row >= mine_from && nl[row] != -INFINITY) part += ex2(fmaf(acc, p.scale_log2, nl[row]));
         }
-        // compensated: many thousand rows may add up
-        const float y = part - carry, t = total + y;
-        carry = (t - total) - y;
-        total = t;
+        add_compensated(total, carry, part);
     }
     if (!mine) return;
     const long long at = ((long long)b * p.Hkv + hk) * kw.ld + j;

@@ -222,9 +222,8 @@ struct Walker {
         return j < s.Lk ? j : -1;
     }
     // first token of row tile r's box of queries: the box ends with the tile, or
-    // starts with the buffer; and the tokens from there to the tile's end
+    // starts with the buffer (then it ends behind the tile)
     __device__ int first_token(int r, int qtile) const { return max(s.Lq - (r + 1) * qtile, -s.q0); }
-    __device__ int tokens(int r, int qtile) const { return s.Lq - r * qtile - first_token(r, qtile); }
     // where the box of packed K starts, in keys from the sequence's first (maybe
     // before it): moved back to end with the sequence, but not before row 0
     __device__ int packed_start(int j0) const { return max(min(j0, s.Lk - kSubKeys), -s.k0); }
@@ -277,8 +276,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
     long long *scan = reinterpret_cast<long long *>(drain + 1);            // [kThreads / 32]
     long long *found = scan + kThreads / 32;                               // [2]
     volatile int *stop = reinterpret_cast<volatile int *>(found + 2);
-    int *skips = reinterpret_cast<int *>(found + 2) + 2;                   // [2] the row tile has rows with lse = -inf
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(found + 2) + 1;
+    int2 *tiles = reinterpret_cast<int2 *>(found + 3);                     // [2] a row tile's first token, and its columns
+                                                                           // (negated: rows with lse = -inf among them)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 for (int i = 0; i < kPer; ++i)
                     if (lane + 32 * i < N)   // a row that saw nothing (lse = -inf) weighs nothing
                         nl[buf * N + lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kLog2e;
-                if (lane == 0) skips[buf] = skip;
+                if (lane == 0) tiles[buf] = make_int2(t0, skip ? (t0 - hi) * G : (hi - t0) * G);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_full[buf]);
             }
@@ -557,9 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 const int buf = j & 1;
                 if (!__all_sync(0xffffffffu, ready) && !(ok = wwait(&s_full[buf], (j >> 1) & 1))) break;
                 tc::fence_after_sync();
-                const int t0 = it.first_token(it.r0 + i, QT);
-                const int cols = min(ncols, it.tokens(it.r0 + i, QT) * G);   // columns of the tile's tokens
-                const bool skip = skips[buf] != 0;
+                const int2 tile = tiles[buf];
+                const int t0 = tile.x, cols = abs(tile.y);
+                const bool skip = tile.y < 0;
                 // every column from `all_from` on sees all of the sub-tile's keys, none
                 // before `any_from` sees any of them
                 const int any_from = max(0, max(-t0, j0 - old - t0)) * G;
@@ -598,10 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&l_empty[buf]);
                 const float2 s2 = fadd2(acc[0], acc[1]);
-                // compensated: many row tiles may add up
-                const float y = (s2.x + s2.y) - carry, t = total + y;
-                carry = (t - total) - y;
-                total = t;
+                add_compensated(total, carry, s2.x + s2.y);
             }
             if (!ok) break;
             if (L::kColHalves == 2 && n > 0) {
@@ -660,9 +657,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
 template <int D, int N>
 constexpr size_t smem_need() {
     using L = Layout<D, N>;
-    // alignment slack, rings, normalisers, sums, barriers, scan, found, flags
+    // alignment slack, rings, normalisers, sums, barriers, scan, found, flags and row tiles
     const size_t need = 1024 + (size_t)L::kKStages * L::kSub + (size_t)L::kQStages * L::kQ + 2 * N * 4 +
-                        kSumSlots * kItemKeys * 4 + (2 * L::kKStages + 2 * L::kQStages + kSumSlots + 7) * 8 + (kThreads / 32 + 2) * 8 + 16;
+                        kSumSlots * kItemKeys * 4 + (2 * L::kKStages + 2 * L::kQStages + kSumSlots + 7) * 8 + (kThreads / 32 + 2) * 8 + 24;
     return need > kMinSmem ? need : kMinSmem;
 }
 
