@@ -109,3 +109,20 @@ def test_infinite_sums_stay_infinite(Hq, Hkv, max_q, paged):
         old = int(lk[b] - lq[b])
         assert torch.equal(out[b, :, :old], w[b, :, :old]) and (out[b, :, old:lk[b]] == 0).all()
     assert plan.check_error() == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,max_q", [(8, 2, 1), (8, 2, 40), (4, 1, 300), (136, 1, 40)])
+def test_infinite_normalisers(Hq, Hkv, max_q):
+    """lse = +inf (a key scored inf): exp(s - inf) is 0 for every finite score
+    and NaN for the infinite one, in tiles that the mask cuts as in whole ones."""
+    lk, lq = 700, max_q
+    q = _bf16((lq, Hq, 64), 1).abs() + 0.1                       # every product with the bad keys is +inf
+    k = _bf16((lk, Hkv, 64), 2)
+    bad = [0, 300, lk - lq]                                       # seen by every query
+    k[bad] = math.inf
+    plan = Plan(1, lk, Hq, Hkv, 64, max_q)
+    lse = torch.full((lq, Hq), math.inf, device="cuda")
+    out = plan.key_weights(q, k, _cu([lq]), _cu([lk]), lse)[0]
+    rest = torch.ones(lk, dtype=torch.bool, device="cuda")
+    rest[bad] = False
+    assert out[:, bad].isnan().all() and (out[:, rest] == 0).all()

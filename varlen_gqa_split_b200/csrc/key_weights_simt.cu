@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kKeys) key_weights_simt_kernel(const Params p,
         if (tid < nr) {
             const long long tok = q0 + (r + tid) / G;
             const float l = __ldg(p.lse + tok * p.Hq + hk * G + (int)((r + tid) % G));
-            nl[tid] = l == -INFINITY ? -INFINITY : -l * kLog2e;   // a row that saw nothing weighs nothing
+            nl[tid] = -l * kLog2e;
         }
         __syncthreads();
         float part = 0.f;
@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(kKeys) key_weights_simt_kernel(const Params p,
                 acc = fmaf(bf16lo(kv[i].w), y.z, acc);
                 acc = fmaf(bf16hi(kv[i].w), y.w, acc);
             }
-            if (mine && r + row >= mine_from && nl[row] != -INFINITY) part += ex2(fmaf(acc, p.scale_log2, nl[row]));
+            // (a row that saw nothing, lse = -inf, weighs nothing)
+            if (mine && r + row >= mine_from && nl[row] != INFINITY) part += ex2(fmaf(acc, p.scale_log2, nl[row]));
         }
         add_compensated(total, carry, part);
     }

@@ -248,9 +248,9 @@ __device__ __forceinline__ void add_columns(const uint32_t (&v)[16], const float
             const float2 t = ffma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), scale,
                                    h ? make_float2(l.z, l.w) : make_float2(l.x, l.y));
             float2 e = make_float2(ex2(t.x), ex2(t.y));
-            if (MASKED) {                     // a row with lse = -inf counts for nothing, whatever its score
-                if (!(vis >> c & 1u) || (h ? l.z : l.x) == -INFINITY) e.x = 0.f;
-                if (!(vis >> (c + 1) & 1u) || (h ? l.w : l.y) == -INFINITY) e.y = 0.f;
+            if (MASKED) {                     // a row with lse = -inf (nl = inf) counts for nothing, whatever its score
+                if (!(vis >> c & 1u) || (h ? l.z : l.x) == INFINITY) e.x = 0.f;
+                if (!(vis >> (c + 1) & 1u) || (h ? l.w : l.y) == INFINITY) e.y = 0.f;
             }
             acc[h] = fadd2(acc[h], e);
         }
@@ -515,8 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_tc_kernel(const __gri
                     break;
 #pragma unroll
                 for (int i = 0; i < kPer; ++i)
-                    if (lane + 32 * i < N)   // a row that saw nothing (lse = -inf) weighs nothing
-                        nl[buf * N + lane + 32 * i] = v[i] == -INFINITY ? -INFINITY : -v[i] * kLog2e;
+                    if (lane + 32 * i < N) nl[buf * N + lane + 32 * i] = -v[i] * kLog2e;
                 if (lane == 0) tiles[buf] = make_int2(t0, skip ? (t0 - hi) * G : (hi - t0) * G);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_full[buf]);
