@@ -190,10 +190,33 @@ def _made(stream, make, *args, **kw):
     other stream while the kernel still writes it."""
     if stream is None:
         return make(*args, **kw)
+    with _on(stream):
+        return make(*args, **kw)
+
+
+def _on(stream):
+    """The context in which `stream` (torch's, or anything with a cuda_stream) is the current one."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream)
-    with torch.cuda.stream(stream):
-        return make(*args, **kw)
+    return torch.cuda.stream(stream)
+
+
+class _Turn(torch.autograd.Function):
+    """A recorded rotation; its backward is the transpose (which is recorded in turn)."""
+
+    @staticmethod
+    def forward(ctx, x, pos, rope, grad):
+        ctx.save_for_backward(pos)
+        ctx.rope, ctx.grad = rope, grad
+        return rope._launch(x, pos, None, grad, None)
+
+    @staticmethod
+    def backward(ctx, g):
+        T, H, D = g.shape
+        # a gradient may come expanded or permuted
+        if (D > 1 and g.stride(2) != 1) or (H > 1 and g.stride(1) != D) or (T > 1 and g.stride(0) < H * D):
+            g = g.contiguous()
+        return ctx.rope.apply(g, *ctx.saved_tensors, grad=not ctx.grad), None, None, None
 
 
 def rope_table(n_pairs, sections=None, *, base=10000.0, restart=False):
@@ -248,7 +271,19 @@ class Rope:
         (bf16, fp16 or fp32; heads contiguous within a token, token stride
         free) by pos [n_axes, T] int32.  grad=True applies the transpose: x is
         the gradient of a rotated tensor, out that of its input.  out may be x
-        itself; it is allocated packed when not given."""
+        itself; it is allocated packed when not given.  Where x requires grad,
+        the rotation is recorded for autograd (not with out)."""
+        grad = bool(grad)
+        if torch.is_grad_enabled() and (getattr(x, "requires_grad", False) or getattr(out, "requires_grad", False)):
+            if out is not None:
+                raise ValueError("out records no gradient: leave it out, or call under no_grad")
+            if stream is None:
+                return _Turn.apply(x, pos, self, grad)
+            with _on(stream):
+                return _Turn.apply(x, pos, self, grad)
+        return self._launch(x, pos, out, grad, stream)
+
+    def _launch(self, x, pos, out, grad, stream):
         if self._h is None:
             raise AttnError(-3, "attn_rope_apply")
         if out is None:
@@ -279,7 +314,8 @@ class Plan:
     keyword choices override the planner (0 = its own; deterministic=1 asks
     for static tile shares, -1 for run-time balancing of shared units;
     wait_limit_us bounds one device wait; test_stall=1 is the test hook of
-    attn_overrides that makes the first call's merge waits run out)."""
+    attn_overrides that makes the first call's merge waits run out).  Its calls
+    are for inference: autograd does not record them."""
 
     def __init__(self, B_max, s_max, Hq, Hkv, D, max_q=1, *, nsplit=0, block_n=0, variant=0,
                  stages=0, combine=0, ctas=0, deterministic=0, wait_limit_us=0, test_stall=0):

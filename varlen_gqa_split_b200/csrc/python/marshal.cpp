@@ -11,6 +11,7 @@
 
 #include <algorithm>
 #include <exception>
+#include <initializer_list>
 
 #include "../../../include/varlen_gqa.h"
 
@@ -144,10 +145,19 @@ struct CacheArgs {
 bool given(PyObject *o) { return o != Py_None; }
 
 // The C ABI call without the interpreter lock, its code as a Python integer.
-template <typename F> PyObject *call(F f) {
+// `written` (tensors or None) count as changed in place, so that autograd
+// notices where it had saved one.
+template <typename F> PyObject *call(std::initializer_list<PyObject *> written, F f) {
     int rc;
     Py_BEGIN_ALLOW_THREADS rc = f();
-    Py_END_ALLOW_THREADS return PyLong_FromLong(rc);
+    Py_END_ALLOW_THREADS
+    if (rc == ATTN_OK)
+        for (PyObject *o : written)
+            if (given(o)) {
+                const at::Tensor &t = THPVariable_Unpack(o);
+                if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+            }
+    return PyLong_FromLong(rc);
 }
 
 template <typename F> PyObject *guarded(Py_ssize_t n, Py_ssize_t want, F f) {
@@ -182,7 +192,7 @@ PyObject *rope_apply(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *stream = address(a[8]);
         if (T == 0 || H == 0) return PyLong_FromLong(0);
         if (H > INT32_MAX) refuse(PyExc_ValueError, "x has too many heads");
-        return call([&] { return f_rope(rope, dtype, xp, xs, T, (int)H, pos, ps, grad, op, os, stream); });
+        return call({a[6]}, [&] { return f_rope(rope, dtype, xp, xs, T, (int)H, pos, ps, grad, op, os, stream); });
     });
 }
 
@@ -206,7 +216,7 @@ PyObject *append_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int32_t *cu_q = per_sequence(a[8], "cu_q", p.dev, p.B + 1), *cu_k = per_sequence(a[9], "cu_k", p.dev, p.B + 1);
         void *stream = address(a[13]);
         if (T == 0) return PyLong_FromLong(0);
-        return call([&] {
+        return call({a[5], a[6], a[12]}, [&] {
             return f_append(p.plan, rope, q, qs, k, ks, v, vs, T, pos, ps, q_out, c.k, c.v, c.page_stride, c.token_stride,
                             c.page_size, c.num_pages, c.table, c.bt_stride, cu_q, cu_k, stream);
         });
@@ -237,7 +247,7 @@ PyObject *key_weights(PyObject *, PyObject *const *a, Py_ssize_t n) {
         void *stream = address(a[12]);
         if (given(a[3])) {
             const CacheArgs c(p, a[2], nullptr, a[3]);
-            return call([&] {
+            return call({a[9], a[11]}, [&] {
                 return f_weights_paged(p.plan, q, T, c.k, c.page_stride, c.token_stride, c.page_size, c.num_pages, c.table,
                                        c.bt_stride, cu_q, cu_k, lse, (float)decay, in, out, ld, seen, born, stream);
             });
@@ -246,7 +256,7 @@ PyObject *key_weights(PyObject *, PyObject *const *a, Py_ssize_t n) {
         long long ks;
         const long long T_kv = k0.dim() ? k0.size(0) : 0;
         void *k = heads(a[2], "k", at::kBFloat16, p.dev, T_kv, p.Hkv, p.D, &ks);
-        return call([&] {
+        return call({a[9], a[11]}, [&] {
             return f_weights(p.plan, q, T, k, ks, T_kv, cu_q, cu_k, lse, (float)decay, in, out, ld, seen, born, stream);
         });
     });
@@ -274,7 +284,7 @@ PyObject *evict_paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (sink > INT32_MAX || recent > INT32_MAX || sink < 0 || recent < 0)
             refuse(PyExc_ValueError, "sink and recent must be in [0, 2^31)");
         void *stream = address(a[14]);
-        return call([&] {
+        return call({a[5], a[6], a[11], a[12], a[13]}, [&] {
             return f_evict(p.plan, w, born, seen, keep, (int)sink, (int)recent, w_out, born_out, shape[2], c.k, c.v,
                            c.page_stride, c.token_stride, c.page_size, c.num_pages, c.table, c.bt_stride, cu_k, cu_out,
                            stream);
