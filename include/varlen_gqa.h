@@ -430,7 +430,7 @@ typedef struct attn_rope_s *attn_rope_t;   /* opaque */
  *   n_pairs  rotated pairs, 1..D/2; elements [2 n_pairs, D) are left as they are
  *   n_axes   position axes, 1..8
  *   freq     host, [n_pairs]: radians per unit of position, finite (64-bit:
- *            the angle of a far position is reduced exactly, see attn_rope_apply)
+ *            whole turns drop out exactly, see attn_rope_apply)
  *   axis     host, [n_pairs]: which axis turns pair i, in [0, n_axes)
  *   layout   ATTN_ROPE_HALF or ATTN_ROPE_INTERLEAVED
  *   scale    factor on cosine and sine (1 for a pure rotation), finite
@@ -460,8 +460,9 @@ void attn_rope_destroy(attn_rope_t rope);   /* NULL or an unknown handle is igno
  *
  * Pair (u, w) of token t turns by theta = pos[axis_i, t] freq_i into
  * scale (u cos theta - w sin theta, u sin theta + w cos theta), the sign of
- * theta flipped for grad.  Angles are reduced in 64-bit fixed point, products
- * are formed in fp32 and rounded once.
+ * theta flipped for grad.  Angles are reduced in 64-bit fixed point: theta is
+ * off by at most 2^-60 |pos| rad, whatever freq, plus the 24 bits that its
+ * sine and cosine are taken with; products are formed in fp32 and rounded once.
  */
 int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int64_t x_token_stride, int64_t T, int H,
                     const int32_t *pos, int64_t pos_stride, int grad, void *out, int64_t out_token_stride,

@@ -272,6 +272,17 @@ namespace {
 std::mutex g_mu;
 std::unordered_set<attn_rope_s *> g_ropes;
 
+// The fraction of a turn per unit position in units of 2^-64, rounded.  Whole
+// turns are dropped by the C library's long double sine and cosine, which
+// reduce an argument of any size exactly: the angle comes back from them in
+// [-pi, pi], good to its 64 bits, where the quotient freq / 2 pi would keep 64
+// bits of the whole turns too and lose as many of the fraction.
+unsigned long long turn_of(double freq) {
+    const long double turns = atan2l(sinl(freq), cosl(freq)) / 6.283185307179586476925286766559005768L;
+    const long double f = roundl(ldexpl(turns, 64));                 // in [-2^63, 2^63]
+    return f >= 9223372036854775808.0L ? 1ull << 63 : (unsigned long long)(long long)f;
+}
+
 bool known(attn_rope_s *r) {
     std::lock_guard<std::mutex> lk(g_mu);
     return g_ropes.count(r) != 0;
@@ -297,12 +308,7 @@ ATTN_EXPORT int attn_rope_create(attn_rope_t *out, int D, int n_pairs, int n_axe
     r->tab.n = n_pairs;
     r->tab.scale = scale;
     for (int i = 0; i < n_pairs; ++i) {
-        // fraction of a turn per unit position in units of 2^-64 (long double
-        // carries 64 bits; whole turns drop out)
-        long double t = (long double)freq[i] / 6.283185307179586476925286766559005768L;
-        t -= floorl(t);
-        const long double f = floorl(ldexpl(t, 64) + 0.5L);
-        r->tab.turn[i] = f >= 18446744073709551616.0L ? 0ull : (unsigned long long)f;
+        r->tab.turn[i] = turn_of(freq[i]);
         r->tab.axis[i] = (uint8_t)axis[i];
     }
     try {

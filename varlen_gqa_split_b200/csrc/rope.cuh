@@ -4,11 +4,13 @@
 // Pair i of a head turns by theta = pos[axis_i] * f_i:
 //     (u, w) -> scale (u cos theta - w sin theta, u sin theta + w cos theta).
 // The angle is kept in turns as a 64-bit fixed-point fraction: with
-// F_i = round(f_i / 2 pi * 2^64) mod 2^64, the product pos * F_i mod 2^64 is
-// the exact fraction of a turn for the rounded F_i, since whole turns wrap
-// away by themselves.  |pos| < 2^31 makes its error at most 2^-34 turns
-// (4e-10 rad) at any distance; an angle in 32-bit floating point would be off
-// by 0.06 rad at position 2^20.  The fraction's upper 32 bits then go to
+// F_i = f_i / 2 pi * 2^64 mod 2^64, the product pos * F_i mod 2^64 is the exact
+// fraction of a turn for this F_i, since whole turns wrap away by themselves.
+// F_i is off by at most 2 units whatever the size of f_i (half a unit of
+// rounding; three long double results of 64 bits before it), so the product by
+// at most 2^-63 |pos| turns: 2^-32 turns (1.5e-9 rad) at the farthest
+// positions.  An angle in 32-bit floating point would be off by 0.06 rad at
+// position 2^20.  The fraction's upper 32 bits then go to
 // sincospif, whose argument in half turns has 24 significant bits: an error
 // of at most pi 2^-25 = 9.4e-8 rad, below the rounding of cos and sin to fp32
 // near one and far below that of the 16-bit types.
