@@ -461,8 +461,8 @@ void attn_rope_destroy(attn_rope_t rope);   /* NULL or an unknown handle is igno
  * Pair (u, w) of token t turns by theta = pos[axis_i, t] freq_i into
  * scale (u cos theta - w sin theta, u sin theta + w cos theta), the sign of
  * theta flipped for grad.  Angles are reduced in 64-bit fixed point: theta is
- * off by at most 2^-60 |pos| rad, whatever freq, plus the 24 bits that its
- * sine and cosine are taken with; products are formed in fp32 and rounded once.
+ * off by at most 2^-60 |pos| rad, whatever freq, its sine and cosine by another
+ * 1.6 * 2^-24; products are formed in fp32 and rounded once.
  */
 int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int64_t x_token_stride, int64_t T, int H,
                     const int32_t *pos, int64_t pos_stride, int grad, void *out, int64_t out_token_stride,

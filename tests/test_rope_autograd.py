@@ -147,3 +147,31 @@ def test_closed_table_in_backward():
     rope.close()
     with pytest.raises(vg.AttnError):
         y.backward()
+
+
+@pytest.mark.gpu
+def test_cosines_and_sines_of_far_positions():
+    """Pairs (1, 0) turn into (cos, sin) themselves, in fp32 within 1.6 * 2^-24
+    (a unit of the library's functions, half a one of a sum, 2 pi 2^-34 rad of
+    the angle) and what 2^-60 |pos| rad of the angle and its 64-bit reference
+    (pos freq off by 2^-53 of itself) are off by."""
+    n = 32
+    freqs = [1e4 ** (-i / n) for i in range(n)]
+    rope = Rope(2 * n, freqs)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    pos = torch.randint(-(1 << 20), 1 << 20, (1, 20000), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.zeros(20000, 1, 2 * n, device="cuda")
+    x[..., :n] = 1.0
+    out = rope.apply(x, pos)[:, 0].double()
+    theta = pos.double().t() * torch.tensor(freqs, dtype=torch.float64, device="cuda")
+    bound = 1.6 * 2.0 ** -24 + 2.0 ** 20 * (2.0 ** -60 + 2.0 ** -52)
+    assert (out[:, :n] - torch.cos(theta)).abs().max() <= bound
+    assert (out[:, n:] - torch.sin(theta)).abs().max() <= bound
+    back = rope.apply(x, pos, grad=True)[:, 0]
+    assert torch.equal(back[:, :n].double(), out[:, :n]) and torch.equal(back[:, n:].double(), -out[:, n:])
+    # quarter turns are exact
+    quarter = Rope(2, [math.pi / 2])
+    y = quarter.apply(torch.tensor([[[1.0, 0.0]]] * 4, device="cuda"), torch.arange(4, dtype=torch.int32, device="cuda")[None])
+    want = torch.tensor([[1.0, 0.0], [0.0, 1.0], [-1.0, 0.0], [0.0, -1.0]], device="cuda")
+    assert (y[:, 0] - want).abs().max() <= 2.0 ** -52

@@ -10,10 +10,11 @@
 // rounding; three long double results of 64 bits before it), so the product by
 // at most 2^-63 |pos| turns: 2^-32 turns (1.5e-9 rad) at the farthest
 // positions.  An angle in 32-bit floating point would be off by 0.06 rad at
-// position 2^20.  The fraction's upper 32 bits then go to
-// sincospif, whose argument in half turns has 24 significant bits: an error
-// of at most pi 2^-25 = 9.4e-8 rad, below the rounding of cos and sin to fp32
-// near one and far below that of the 16-bit types.
+// position 2^20.  Its quarter turns are split off; of the rest,
+// in [-1/8, 1/8] turn, rounded to 33 bits, 24 bits go to sincospif and what they leave,
+// b <= 2^-25 rad, comes in by sin(a + b) = sin a + b cos a.  Cosine and sine are
+// then within 1.6 * 2^-24: one unit of sincospif, half a one of the last sum,
+// and the 34th bit.  (The fraction as one float would cost up to 9.4e-8 rad.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,10 +39,18 @@ struct RopeTable {
 // (scale cos, scale sin) of pair i at `pos` positions; sign -1 turns backwards
 __device__ __forceinline__ float2 rope_cos_sin(const RopeTable &tab, int i, int pos, float sign) {
     const unsigned long long t = (unsigned long long)(long long)pos * tab.turn[i];
-    const int hi = (int)((t + 0x80000000ull) >> 32);          // 2^-32 turns, in [-1/2, 1/2) turn
+    const uint32_t quarter = (uint32_t)((t + (1ull << 61)) >> 62);
+    // 2^-33 turns, rounded, in [-2^30, 2^30]
+    const int rest = (int)((long long)(t - ((unsigned long long)quarter << 62) + (1ull << 30)) >> 31);
+    const float a = (float)rest;
+    const float b = (float)(rest - (int)a) * 7.314590e-10f;   // rad: 2 pi 2^-33
     float s, c;
-    sincospif((float)hi * 4.656612873077393e-10f, &s, &c);    // half turns: hi * 2^-31
-    return make_float2(c * tab.scale, s * tab.scale * sign);
+    sincospif(a * 2.3283064365386963e-10f, &s, &c);           // half turns: 2^-32
+    const float sb = fmaf(b, c, s), cb = fmaf(-b, s, c);
+    const float x = quarter & 1 ? sb : cb, y = quarter & 1 ? cb : sb;
+    // cosine: c, -s, -c, s; sine: s, c, -s, -c
+    const float cosine = (quarter + 1) & 2 ? -x : x, sine = quarter & 2 ? -y : y;
+    return make_float2(cosine * tab.scale, sine * tab.scale * sign);
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
