@@ -1,5 +1,7 @@
 """Binding of libvgqa (include/varlen_gqa.h): argument marshalling only, by
-ctypes and, for the cache operators, by the native module _lib/_marshal.so.
+ctypes and, for the cache operators, by the native module _lib/_marshal.*.so
+(built for one torch and one interpreter, which its name carries; loaded with
+the first of these calls).
 
 Every step of the attention runs in the library's CUDA kernels; this module
 checks dtypes, shapes and devices of torch tensors, passes their device
@@ -13,13 +15,14 @@ import ctypes
 import importlib.machinery
 import importlib.util
 import os
+import sys
 import threading
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libvgqa.so")
-MARSHAL_PATH = os.path.join(_HERE, "_lib", "_marshal.so")
+MARSHAL_PATH = os.path.join(_HERE, "_lib", f"_marshal.{sys.implementation.cache_tag}.torch-{torch.__version__}.so")
 
 ATTN_OK = 0
 ATTN_VARIANT_AUTO, ATTN_VARIANT_SIMT, ATTN_VARIANT_MMA, ATTN_VARIANT_TC = 0, 1, 2, 3
@@ -60,12 +63,33 @@ class AttnError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
-_marshal = None          # native marshalling of the cache operators, loaded with the library
+
+
+class _Unloaded:
+    """Stands for the marshalling module until one of its functions is asked for."""
+
+    def __getattr__(self, name):
+        global _marshal
+        lib()
+        with _lock:
+            if isinstance(_marshal, _Unloaded):
+                if not os.path.exists(MARSHAL_PATH):
+                    raise RuntimeError(f"the cache operators' binding is not built for this torch and interpreter "
+                                       f"({MARSHAL_PATH}); run `python -m varlen_gqa_split_b200.build`")
+                loader = importlib.machinery.ExtensionFileLoader("_marshal", MARSHAL_PATH)
+                m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+                loader.exec_module(m)
+                m.bind(LIB_PATH)
+                _marshal = m
+        return getattr(_marshal, name)
+
+
+_marshal = _Unloaded()   # native marshalling of the cache operators
 
 
 def lib() -> ctypes.CDLL:
     """Load libvgqa.so (raises if it has not been built)."""
-    global _lib, _marshal
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -74,8 +98,6 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"libvgqa.so not built ({LIB_PATH}); run "
                                "`python -m varlen_gqa_split_b200.build`")
-        if not os.path.exists(MARSHAL_PATH):
-            raise RuntimeError(f"_marshal.so not built ({MARSHAL_PATH}); run `python -m varlen_gqa_split_b200.build`")
         L = ctypes.CDLL(LIB_PATH)
         vp, i, i32p = ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p
         L.attn_plan.argtypes = [ctypes.POINTER(vp), i, i, i, i, i, i]
@@ -122,11 +144,6 @@ def lib() -> ctypes.CDLL:
         L.attn_key_weights_paged.restype = i
         L.attn_evict_paged.argtypes = [vp, vp, i32p, i32p, i32p, i, i, vp, i32p, i64, vp, vp] + cache + [i32p, i32p, vp]
         L.attn_evict_paged.restype = i
-        loader = importlib.machinery.ExtensionFileLoader("_marshal", MARSHAL_PATH)
-        m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
-        loader.exec_module(m)
-        m.bind(LIB_PATH)
-        _marshal = m
         _lib = L
         return L
 

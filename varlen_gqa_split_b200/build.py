@@ -27,7 +27,6 @@ LIB = os.path.join(LIBDIR, "libvgqa.so")
 # the binding's native marshalling (a Python extension module; needs torch's
 # headers, calls the library through its C ABI)
 MARSHAL_SRC = os.path.join(CSRC, "python", "marshal.cpp")
-MARSHAL = os.path.join(LIBDIR, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-I", INCLUDE,
@@ -57,9 +56,17 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def marshal_path() -> str:
+    """The module for the torch and the interpreter that run: another torch
+    gets another one."""
+    from ._binding import MARSHAL_PATH
+    return MARSHAL_PATH
+
+
 def marshal_up_to_date() -> bool:
+    path = marshal_path()
     deps = [MARSHAL_SRC, os.path.join(INCLUDE, "varlen_gqa.h"), os.path.abspath(__file__)]
-    return os.path.exists(MARSHAL) and all(os.path.getmtime(f) <= os.path.getmtime(MARSHAL) for f in deps)
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in deps)
 
 
 def build_marshal() -> str:
@@ -69,15 +76,16 @@ def build_marshal() -> str:
     base = os.path.join(os.path.dirname(torch.__file__))
     inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
            os.path.join(base, "include", "torch", "csrc", "api", "include")]
-    tmp = MARSHAL + f".tmp{os.getpid()}"
+    path = marshal_path()
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{d}" for d in inc] + \
         [MARSHAL_SRC, "-o", tmp, "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, path)
+    return path
 
 
 def _compile(src: str, verbose: bool) -> tuple[str, str]:
