@@ -122,3 +122,11 @@ def test_programmatic_dependents_read_by_plain_loads():
         text = re.sub(r"//[^\n]*|/\*.*?\*/", "", open(path).read(), flags=re.S)
         if path.endswith(".cuh") or "ProgrammaticStreamSerialization" in text or "launch_dependent(" in text:
             assert not re.search(r"__ldg\s*\(|ld\.global(\.\w+)*\.nc\b|__restrict__", text), os.path.basename(path)
+
+
+def test_launch_rules_ask_the_device_for_its_sms():
+    """No rule holds the SM count of one card as a number."""
+    csrc = os.path.join(ROOT, "varlen_gqa_split_b200", "csrc")
+    for path in sorted(glob.glob(os.path.join(csrc, "*.*"))):
+        text = re.sub(r"//[^\n]*|/\*.*?\*/", "", open(path).read(), flags=re.S)
+        assert not re.search(r"\b148\b", text), os.path.basename(path)

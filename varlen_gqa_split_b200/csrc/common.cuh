@@ -134,7 +134,8 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
     float2 d;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
     return d;
-}__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+}
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);   // .x (low half) = lo
     return *reinterpret_cast<uint32_t *>(&h);
 }

@@ -506,12 +506,12 @@ cudaError_t evict_prepare() {
 
 namespace {
 
-cudaError_t launch_evict(const Params &p, Evict e, cudaStream_t stream) {
+cudaError_t launch_evict(const Params &p, Evict e, int sms, cudaStream_t stream) {
     // A cluster per unit: as many blocks as fill the device, but no slice
     // under 1024 keys (8 units of 32768 keys: 8 blocks each 18.9 us; 4 took 29.4 where 8 took 19.9)
     const long long units = (long long)p.B_max * p.Hkv;
     int cs = 1;
-    while (cs < kMaxCluster && units * cs * 2 <= 148 * kBlocksPerSm && p.s_max >= 2048 * cs) cs *= 2;
+    while (cs < kMaxCluster && units * cs * 2 <= sms * kBlocksPerSm && p.s_max >= 2048 * cs) cs *= 2;
     e.slice_words = slice_words(p.s_max, cs);
     const size_t fixed = sizeof(Head) + bits_bytes(p.s_max, cs), ranks = (size_t)e.slice_words * 32 * 4;
     e.cached = fixed + ranks <= (size_t)kMaxSmem ? e.slice_words * 32 : 0;
@@ -585,5 +585,5 @@ ATTN_EXPORT int attn_evict_paged(attn_plan_t plan, const float *weight, const in
     e.ld = ld;
     e.sink = sink;
     e.recent = recent;
-    return launch_evict(p, e, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_E_CUDA;
+    return launch_evict(p, e, d.num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? ATTN_OK : ATTN_E_CUDA;
 }

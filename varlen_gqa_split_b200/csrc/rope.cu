@@ -13,6 +13,7 @@
 // HBM bandwidth (8 heads a thread, two in flight: 55.9; 16: 62); 64 tokens x
 // 40 heads 2.9 us; four chunks of 512 to 2048 tokens appended 25.3 us, 63%.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <mutex>
 #include <new>
@@ -49,10 +50,10 @@ struct Shape {
 
 // Heads per thread: enough work to keep the factors' cost small, but a thread
 // per head while the whole call would not fill the device twice over.
-Shape shape_of(long long n_tok, int heads, int groups, int n, int most) {
+Shape shape_of(long long n_tok, int heads, int groups, int n, int most, int sms) {
     Shape s;
     s.groups = groups;
-    const long long fill = 2ll * 148 * kThreads * kBlocksPerSm;
+    const long long fill = 2ll * sms * kThreads * kBlocksPerSm;
     const int each = (int)std::max(1ll, std::min<long long>(most, n_tok * heads * groups / fill));
     s.lanes = std::min((heads + each - 1) / each, kThreads / groups);
     s.tokens = std::max(1, std::min(kThreads / (groups * s.lanes), kMaxFactors / std::max(n, 1)));
@@ -60,6 +61,18 @@ Shape shape_of(long long n_tok, int heads, int groups, int n, int most) {
     s.threads = (s.tokens * groups * s.lanes + 31) / 32 * 32;
     s.blocks = (n_tok + s.tokens - 1) / s.tokens;
     return s;
+}
+
+// SMs of the current device (asked once per device)
+int current_sms() {
+    static std::atomic<int> known[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    std::atomic<int> *at = dev < 64 ? &known[dev] : nullptr;
+    if (at && (sms = at->load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    if (at) at->store(sms, std::memory_order_relaxed);
+    return sms;
 }
 
 // the cosines and sines of tokens [t0, t0 + nt): cs[token][pair]
@@ -239,7 +252,7 @@ int access_width(int size, int n, int D, uintptr_t bits) {
 template <typename T, int V>
 cudaError_t launch_rope(const attn_rope_s &r, const void *x, long long xs, long long n_tok, int H, const int32_t *pos,
                         long long ps, bool grad, void *out, long long os, cudaStream_t s) {
-    const Shape sh = shape_of(n_tok, H, rope_groups(r.tab.n, r.D, V), r.tab.n, kMaxHeads);
+    const Shape sh = shape_of(n_tok, H, rope_groups(r.tab.n, r.D, V), r.tab.n, kMaxHeads, current_sms());
     if (sh.blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     const size_t smem = (size_t)sh.tokens * r.tab.n * sizeof(float2);
     auto *fn = r.layout == ATTN_ROPE_HALF ? rope_kernel<T, V, true> : rope_kernel<T, V, false>;
@@ -249,9 +262,9 @@ cudaError_t launch_rope(const attn_rope_s &r, const void *x, long long xs, long 
 }
 
 template <int V>
-cudaError_t launch_append(const RopeTable &tab, bool half, const Params &p, Append ap, cudaStream_t s) {
+cudaError_t launch_append(const RopeTable &tab, bool half, const Params &p, Append ap, int sms, cudaStream_t s) {
     const Shape sh = shape_of(ap.n_tok, (ap.q_out ? p.Hq : 0) + 2 * p.Hkv, rope_groups(tab.n, p.D, V), tab.n,
-                              kAppendHeads);
+                              kAppendHeads, sms);
     if (sh.blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     ap.groups = sh.groups;
     ap.lanes = sh.lanes;
@@ -449,8 +462,8 @@ ATTN_EXPORT int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void
     // strides and pointers are 16-byte ones here; only the pair count may be odd
     const int w = access_width(2, tab.n, d.D, 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = w == 8   ? launch_append<8>(tab, half, p, ap, s)
-                          : w == 4 ? launch_append<4>(tab, half, p, ap, s)
-                                   : launch_append<1>(tab, half, p, ap, s);
+    const cudaError_t e = w == 8   ? launch_append<8>(tab, half, p, ap, d.num_sms, s)
+                          : w == 4 ? launch_append<4>(tab, half, p, ap, d.num_sms, s)
+                                   : launch_append<1>(tab, half, p, ap, d.num_sms, s);
     return e == cudaSuccess ? ATTN_OK : ATTN_E_CUDA;
 }
