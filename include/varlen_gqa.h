@@ -483,8 +483,8 @@ int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int64_t x_token_
  *   T_q      rows of q, k, v and pos, >= cu_q[B_max] (a sequence past them is
  *            an error of its offsets)
  *   q_out    device, bf16 [T_q, Hq, D] packed, 16-byte aligned: the rotated
- *            queries, ready for attn_run_paged.  q itself where q is packed,
- *            or apart from q, k and v
+ *            queries, ready for attn_run_paged.  q itself where q is packed
+ *            (and k and v lie apart from it), or apart from q, k and v
  *   pos      as in attn_rope_apply, for the T_q tokens
  *   k_cache .. bt_stride  as in attn_run_paged
  *   cu_q, cu_k  as in attn_run_paged: cu_k's lengths COUNT the new tokens, and
@@ -494,7 +494,8 @@ int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int64_t x_token_
  * plan's bounds sets the plan's sticky bit and nothing of it is written; a
  * block-table entry outside the cache sets ATTN_DEV_ERR_PAGE and its keys are
  * not stored; tokens with a negative key index (Lq_b > Lk_b) are rotated but
- * not stored.  Two sequences must not share the pages that are written.
+ * not stored.  Two sequences must not share the pages that are written, and
+ * none of q, k, v and pos may lie in the rows that are.
  */
 int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void *q, int64_t q_token_stride, const void *k,
                       int64_t k_token_stride, const void *v, int64_t v_token_stride, int64_t T_q, const int32_t *pos,

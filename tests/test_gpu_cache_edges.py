@@ -126,3 +126,24 @@ def test_infinite_normalisers(Hq, Hkv, max_q):
     rest = torch.ones(lk, dtype=torch.bool, device="cuda")
     rest[bad] = False
     assert out[:, bad].isnan().all() and (out[:, rest] == 0).all()
+
+
+# ------------------------------------------------------- overlaps and strides
+
+def test_append_in_place_refuses_shared_rows():
+    """q_out may be q itself only where no key or value is read from it: they
+    would be read after the rotated queries were written."""
+    plan, rope = Plan(1, 64, 4, 4, 64, 8), Rope(64, *rope_table(32))
+    q, k = _bf16((8, 4, 64), 1), _bf16((8, 4, 64), 2)
+    kc, vc = (torch.zeros(4, 16, 4, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    bt, pos = torch.arange(4, dtype=torch.int32, device="cuda")[None], torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    cu = _cu([8])
+    was = q.clone()
+    for k_, v_ in ((q, k), (k, q), (q, q)):
+        with pytest.raises(vg.AttnError):
+            plan.append_paged(k_, v_, kc, vc, bt, cu, cu, q=q, pos=pos, rope=rope, q_out=q)
+    torch.cuda.synchronize()
+    assert torch.equal(q, was) and not kc.any()
+    plan.append_paged(q, k, kc, vc, bt, cu, cu, q=q, pos=pos, rope=rope)      # apart: allowed
+    assert plan.append_paged(k, k, kc, vc, bt, cu, cu, q=q, pos=pos, rope=rope, q_out=q) is q
+    assert torch.equal(q, rope.apply(was, pos)) and plan.check_error() == 0

@@ -419,7 +419,7 @@ ATTN_EXPORT int attn_append_paged(attn_plan_t plan, attn_rope_t rope, const void
             return a < b + T_q * qrow * 2 && b < a + ((T_q - 1) * stride + row) * 2;
         };
         if (q_out == q ? q_token_stride != qrow : overlaps(q, q_token_stride, qrow)) return ATTN_E_INVALID_ARG;
-        if (q_out != q && (overlaps(k, k_token_stride, krow) || overlaps(v, v_token_stride, krow))) return ATTN_E_INVALID_ARG;
+        if (overlaps(k, k_token_stride, krow) || overlaps(v, v_token_stride, krow)) return ATTN_E_INVALID_ARG;
     }
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return ATTN_E_CUDA;
