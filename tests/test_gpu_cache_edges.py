@@ -147,3 +147,22 @@ def test_append_in_place_refuses_shared_rows():
     plan.append_paged(q, k, kc, vc, bt, cu, cu, q=q, pos=pos, rope=rope)      # apart: allowed
     assert plan.append_paged(k, k, kc, vc, bt, cu, cu, q=q, pos=pos, rope=rope, q_out=q) is q
     assert torch.equal(q, rope.apply(was, pos)) and plan.check_error() == 0
+
+
+def test_a_single_token_needs_no_token_stride():
+    """One token of a buffer whose token stride no call could use (odd, or
+    smaller than a token): the stride is never followed."""
+    D, Hq, Hkv = 64, 4, 2
+    plan, rope = Plan(1, 64, Hq, Hkv, D, 1), Rope(D, *rope_table(32))
+    pos, cu = torch.tensor([[7]], dtype=torch.int32, device="cuda"), _cu([1])
+    bt = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    for stride in (Hq * D + 4, 3, 0):
+        q, k, v = (torch.as_strided(_bf16((1000,), i), (1, h, D), (stride, D, 1)) for i, h in ((1, Hq), (2, Hkv), (3, Hkv)))
+        assert torch.equal(rope.apply(q, pos), rope.apply(q.contiguous(), pos))
+        kc, vc = (torch.zeros(4, 16, Hkv, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        qo = plan.append_paged(k, v, kc, vc, bt, cu, cu, q=q, pos=pos, rope=rope)
+        assert torch.equal(qo, rope.apply(q, pos)) and torch.equal(kc[0, 0], rope.apply(k, pos)[0])
+        assert torch.equal(vc[0, 0], v[0])
+        lse = torch.zeros(1, Hq, device="cuda")
+        w = plan.key_weights(qo, k, cu, cu, lse)
+        assert torch.equal(w, plan.key_weights(qo, k.contiguous(), cu, cu, lse))

@@ -52,7 +52,8 @@ const at::Tensor &tensor(PyObject *o, const char *name, at::ScalarType type, lon
     return t;
 }
 
-// [T, H, D] with the heads contiguous within a token; *stride is the tokens'
+// [T, H, D] with the heads contiguous within a token; *stride is the tokens' (a
+// single token has none that matters)
 void *heads(PyObject *o, const char *name, at::ScalarType type, long long dev, long long T, long long H, long long D,
             long long *stride) {
     const at::Tensor &t = tensor(o, name, type, dev);
@@ -60,7 +61,7 @@ void *heads(PyObject *o, const char *name, at::ScalarType type, long long dev, l
         refuse(PyExc_ValueError, "%s must be [%lld, %lld, %lld]", name, T, H, D);
     if ((D > 1 && t.stride(2) != 1) || (H > 1 && t.stride(1) != D))
         refuse(PyExc_ValueError, "%s must keep each token's heads contiguous (strides (s, D, 1), s >= H*D)", name);
-    *stride = T > 1 ? t.stride(0) : std::max<long long>(t.stride(0), H * D);
+    *stride = T > 1 ? (long long)t.stride(0) : H * D;
     return t.data_ptr();
 }
 
