@@ -454,7 +454,7 @@ void attn_rope_destroy(attn_rope_t rope);   /* NULL or an unknown handle is igno
  *            widest accesses).  out may be x itself (same stride) or lie apart
  *            from it; any other overlap is ATTN_E_INVALID_ARG
  *   pos      device, int32, position of token t on axis a at pos[a * pos_stride
- *            + t]; any value, negative ones too; pos_stride >= T
+ *            + t]; any value, negative ones too; pos_stride >= T; apart from out
  *   grad     0: out = R x.  1: out = R^T x, the gradient with respect to the
  *            input for a gradient x with respect to the output
  *

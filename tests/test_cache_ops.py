@@ -146,3 +146,12 @@ def test_rope_table_turns_are_exact_for_frequencies_of_any_size(L):
         off = (got - exact) % (1 << 64)
         assert min(off, (1 << 64) - off) <= 2 + 1, f                    # 2 units, and the floor's one
     L.attn_rope_destroy(h)
+
+
+def test_rope_positions_lie_apart_from_the_result(L):
+    rc, h = _create(L)                                       # D = 8, two axes, T = 4, H = 2: out is 128 bytes, pos 32
+    assert rc == OK
+    for pos in (0x20000, 0x20000 + 124, 0x20000 - 28, 0x20000 - 32 + 4):
+        assert _apply(L, h, pos=pos) == INVALID
+    assert _apply(L, h, pos=0x20000, x=0x20000, T=0) == OK   # nothing is read or written
+    L.attn_rope_destroy(h)

@@ -368,6 +368,11 @@ ATTN_EXPORT int attn_rope_apply(attn_rope_t rope, int dtype, const void *x, int6
         if (x_token_stride != out_token_stride || gap < row * size || x_token_stride * size - gap < row * size)
             return ATTN_E_INVALID_ARG;
     }
+    // the positions are read while rows are written
+    const char *pb = reinterpret_cast<const char *>(pos);
+    if (pb < ob + ((T - 1) * out_token_stride + row) * size &&
+        ob < pb + ((rope->n_axes - 1) * (rope->n_axes > 1 ? pos_stride : 0) + T) * 4)
+        return ATTN_E_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const uintptr_t bits = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(out) |
                            (uintptr_t)(x_token_stride * size) | (uintptr_t)(out_token_stride * size);
