@@ -24,10 +24,12 @@
 //      and of kept keys above, prefix-summed;
 //   4. the moves: pair i finds its place and its key by binary search in
 //      those counts, and 16 bytes a thread go from row to row.
-// Small cuts take the latency of those steps (64 sequences x 8 heads of 1044
-// keys cut to 1024: 13.2 us; 8 heads of 32768 keys to 2048: 18.9), large ones
-// the bandwidth of the moved rows (64 x 8 heads of up to 8192 keys to 1024:
-// 78.5 us, 82% of the measured HBM bandwidth).
+// Small cuts take the latency of those steps, one wave of blocks after the other
+// (8 heads of 1044 keys cut to 1024: 48 sequences 10.8 us, 55, the last that three
+// blocks an SM hold at once, 11.3, 64 13.4, 72 16.9; 8 heads of 32768 keys to
+// 2048: 18.8, 64 blocks in all), large ones the bandwidth of the moved rows (64
+// x 8 heads of up to 8192 keys to 1024: 78 to 82 us, 79 to 83% of the measured
+// HBM bandwidth).
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -18,10 +18,11 @@
 // parts, 256 sums each, are added in block order by whichever block finishes
 // last.  Decode has one row tile per item: no cuts, K streams through.
 //
-// Measured: 64 ragged sequences of a decode step (8 KV heads, 554 MB) 91 to 94
-// us, 90 to 93% of the measured HBM bandwidth; 2 x 1025..2048 tokens over 24k..32k keys,
-// 64 heads, 1.67 to 1.79 ms, 0.5 of the measured tensor rate: the exponentials need
-// 1.2 ms of the special-function unit (79% busy).
+// Measured: 64 ragged sequences of a decode step (8 KV heads, 554 MB) 87 to 96
+// us, 88 to 97% of the measured HBM bandwidth (from 64-key pages 111 us for 97,
+// from 8-key pages 222); 2 x 1025..2048 tokens over 24k..32k keys, 64 heads, 1.65
+// to 2.0 ms by their lengths and the power cap, half of the measured tensor rate:
+// the exponentials need 1.2 ms of the special-function unit (79% busy).
 //
 // Warps: 0-15 epilogue (warp w: sub-tile w / 4 mod 2, lanes 32 (w mod 4), and
 // of the columns, where there are 64 or more, half w / 8: four warps a

@@ -9,9 +9,11 @@
 // about 40 instructions a pair), and a thread keeps those of its token and its
 // V pairs in registers while it goes through some of the token's heads: two
 // 16-byte loads and two 16-byte stores a head, several heads in flight.
-// Measured: 8192 tokens x 72 heads of 128, bf16, 48.0 us, 96% of the measured
+// Measured: 8192 tokens x 72 heads of 128, bf16, 48.3 us, 96% of the measured
 // HBM bandwidth (8 heads a thread, two in flight: 55.9; 16: 62); 64 tokens x
-// 40 heads 2.9 us; four chunks of 512 to 2048 tokens appended 25.3 us, 63%.
+// 40 heads 2.9 us; four chunks of 512 to 2048 tokens of 2048 rows each appended
+// 24.5 to 25.8 us, 62 to 66% (a block whose rows lie behind the last sequence
+// finds that out only after its factors: with all 8192 rows live 33.2, 77%).
 #include <algorithm>
 #include <atomic>
 #include <cmath>

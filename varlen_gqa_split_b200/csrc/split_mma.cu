@@ -316,10 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1) split_mma_kernel(const __grid_con
         // The box of a packed sequence of less than a tile holds rows of others.
         // This warp zeroes its rows of them in V: their weights are 0, but 0
         // times a non-finite value would not be (rows outside the buffer came
-        // as zeros).  The unit has this one tile.  (256 sequences of 40 keys, 8 KV heads: 36.5 -> 38.5 us a call;
-        // inside the loop it would cost every batch 1 to 2%, and a producer
-        // that waits for such a tile and zeroes costs 2% of a ragged batch with
-        // two such sequences.)
+        // as zeros).  The unit has this one tile.  (256 sequences of 40 keys, 8
+        // KV heads: 36.5 -> 38.5 us a call; inside the loop it would cost every
+        // batch 1 to 2%, and a producer that waits for such a tile and zeroes
+        // costs 2% of a ragged batch with two such sequences.)
         const int last = last_start(p, Lk, cur.s.k0);
         if (!PAGED && Lk < kBN && (cur.s.k0 > 0 || p.rows_kv != kRowsOpen) && mbar_wait(&full[s], phase, p.wait_ns) &&
             !(meta[s].y & kMetaEmpty)) {

@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1) split_tc_kernel(const __grid_cons
     // previous kernel in the stream still runs.  Meanwhile it prefetches its
     // first K/V tiles into L2 under a speculative schedule (the warp-MMA
     // kernel does the same; both are hints that no later write can make
-    // stale, and stay in rows that are known to be there).  Then it waits for that kernel before the reads that count;
-    // only then may this call's combine kernel launch.
+    // stale, and stay in rows that are known to be there).  Then it waits for
+    // that kernel before the reads that count; only then may this call's
+    // combine kernel launch.
     if constexpr (!PAGED) {
         Share sp;
         if (block_share(p, c, gridDim.x, tid, kThreads, false, scan, first, sp, true) && warp == kProducerWarp)
